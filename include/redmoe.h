@@ -302,6 +302,139 @@ redmoe_status redmoe_forward_stack(const redmoe_layer *layers, int32_t n_layers,
 redmoe_status redmoe_forward_noalloc(const redmoe_layer *L, const void *x, int32_t T, float *out,
                                      int32_t *topk_ids, float *topk_w, void *stream);
 
+/* ---------------------------------------------------------------------------------
+ * The step between blocks: norms, gate and residual around the layer.
+ *
+ * N(v; w) = v / sqrt(mean(v^2) + eps) * (w_offset + w), over the hidden elements of one
+ * token row (RMS norm); where a weight pointer is NULL the factor is 1. Per row:
+ *
+ *   u     = N(y; post_w)   if post_norm, else y          norm behind the block
+ *   h_out = res_scale * h + block_scale * g * u          residual step
+ *   x     = N(h_out; pre_w)                              norm before the next block
+ *
+ * g is 1 (REDMOE_GATE_NONE), or act(gate) with gate [T] (TOKEN), [hidden] (CHANNEL) or
+ * [T, hidden] (ELEMENT), act the identity (LINEAR) or the logistic function (SIGMOID).
+ * Statistics are fp32; x is computed from h_out before h_out is rounded to h_dtype, so
+ * every output is rounded once. Rows are independent; T = 1 and long batches run the same
+ * kernel. hidden is a multiple of 8 up to 8192 (more: REDMOE_ERR_UNSUPPORTED); dtypes are
+ * REDMOE_F32 or REDMOE_BF16; tensors are 16-byte aligned (a TOKEN gate: to its element).
+ * These operators are this library's own: the pages describe the layers around the MoE
+ * block only by name ("Architecture", "Qwen3-Next shape"). */
+typedef enum {
+    REDMOE_GATE_NONE = 0,
+    REDMOE_GATE_TOKEN = 1,
+    REDMOE_GATE_CHANNEL = 2,
+    REDMOE_GATE_ELEMENT = 3
+} redmoe_gate_kind;
+typedef enum { REDMOE_GATE_LINEAR = 0, REDMOE_GATE_SIGMOID = 1 } redmoe_gate_act;
+
+typedef struct redmoe_norm {
+    int32_t hidden;
+    int32_t h_dtype;         /* of h, h_out and their gradients                               */
+    int32_t y_dtype;         /* of the block's output y and its gradient                      */
+    int32_t x_dtype;         /* of x and its gradient                                         */
+    int32_t w_dtype;         /* of post_w and pre_w                                           */
+    int32_t post_norm;       /* 1: y is normalised; 0: it is not                              */
+    int32_t gate_kind;       /* redmoe_gate_kind                                              */
+    int32_t gate_act;        /* redmoe_gate_act                                               */
+    int32_t gate_dtype;
+    float eps;               /* > 0                                                           */
+    float w_offset;          /* added to every weight: 0, or 1 for weights stored around zero */
+    float res_scale;
+    float block_scale;
+    const void *post_w;      /* [hidden], or NULL (needs post_norm)                           */
+    const void *pre_w;       /* [hidden], or NULL                                             */
+} redmoe_norm;
+
+/* The forward pass for T rows.
+ *   y == NULL: the norm before a block alone, x = N(h; pre_w); gate and h_out are NULL too.
+ *   else: h_out is written, and x where it is not NULL.
+ * h_out may be h itself (in place); no other output may overlap an input or the other
+ * output (REDMOE_ERR_INVALID_ARG). T == 0 is a valid empty call. */
+redmoe_status redmoe_norm_forward(const redmoe_norm *N, const void *h, const void *y, const void *gate, int32_t T,
+                                  void *h_out, void *x, void *stream);
+
+/* The backward pass: gradients of h, y, gate and both weights from the stored h_out (for
+ * y == NULL: the h that was normalised), y and gate, and the gradients dh_out and dx that
+ * arrive at h_out and x. Either of those may be NULL (zero), not both.
+ *   dh       [T, hidden] h_dtype; may be dh_out itself
+ *   dy       [T, hidden] y_dtype, required with y
+ *   dgate    TOKEN: fp32 [T]; CHANNEL: fp32 [hidden]; ELEMENT: gate_dtype [T, hidden]; NULL:
+ *            not wanted
+ *   dpost_w, dpre_w   fp32 [hidden], 16-byte aligned; NULL: not wanted
+ * Overwritten, not accumulated; sums over rows are fp32 in a fixed order. The workspace is
+ * needed for dpost_w, dpre_w and a CHANNEL dgate (else it may be NULL); its control block
+ * is not used. T == 0 zeroes those three and touches nothing else. */
+size_t redmoe_norm_workspace_bytes(const redmoe_norm *N, int32_t T);
+redmoe_status redmoe_norm_backward(const redmoe_norm *N, const void *h_out, const void *y, const void *gate,
+                                   const void *dh_out, const void *dx, int32_t T, void *dh, void *dy, void *dgate,
+                                   float *dpost_w, float *dpre_w, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* The residual block around the layer, on one stream:
+ *   x = N(h; before->pre_w);  y = layer(x);  h_out, x_next = the step of `after` on (h, y)
+ * `before` is used as in redmoe_norm_forward with y == NULL, `after` as with y. Both have
+ * the layer's hidden; before->x_dtype is the layer's x_dtype, after->y_dtype is REDMOE_F32
+ * (the layer's output) and after->h_dtype is before->h_dtype; otherwise
+ * REDMOE_ERR_INVALID_ARG. h_out may be h itself, x_next may be NULL. Sizes, ids, weights
+ * and statuses as redmoe_forward; the workspace holds redmoe_workspace_bytes_block(L, T)
+ * bytes. If the layer's own dispatch refuses the layer (REDMOE_ERR_UNSUPPORTED) or a launch
+ * fails, the first norm may have been enqueued: it writes the workspace only. */
+size_t redmoe_workspace_bytes_block(const redmoe_layer *L, int32_t T);
+redmoe_status redmoe_forward_block(const redmoe_layer *L, const redmoe_norm *before, const redmoe_norm *after,
+                                   const void *h, const void *gate, int32_t T, void *h_out, void *x_next,
+                                   int32_t *topk_ids, float *topk_w, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * Load balance of a router: per-expert counts, mean probabilities and two losses over the
+ * rows of logits [T, E] (as redmoe_router returns them, or in bf16) and topk_ids [T, k].
+ *
+ * A row counts if its byte in row_mask [T] is not zero (NULL: every row) and its logits are
+ * not all -infinity; what the other rows hold, NaN and ids included, has no effect. With n
+ * the number of rows that count and p = softmax of a row's logits over all E experts:
+ *   counts[e] = ids equal to e                 (ids outside 0 .. E-1 are counted nowhere)
+ *   prob[e]   = (1/n) sum p[t, e]
+ *   loss[0]   = E sum_e counts[e] / (n k) prob[e]    balance loss, 1 at an even load
+ *   loss[1]   = (1/n) sum logsumexp(logits[t])^2     z loss
+ * (n == 0: all zero). Nothing here is scaled by a coefficient: scale the losses, and pass
+ * the coefficients as grad_loss [2] on the way back, where the counts are constants:
+ *   dlogits[t, e] = grad_loss[0] E / (n^2 k) p[t, e] (counts[e] - sum_j p[t, j] counts[j])
+ *                 + grad_loss[1] (2 / n) lse[t] p[t, e];   zero in rows that do not count.
+ * dlogits has the logits' dtype, is overwritten and may be logits itself. counts and n_rows
+ * are those of the forward call. E is 1..1024, k 1..min(E, 32), T k at most 2^30; logits
+ * REDMOE_F32 or REDMOE_BF16, 16-byte aligned. Sums over rows have a fixed order: results do
+ * not depend on timing. Outputs must not overlap inputs or one another
+ * (REDMOE_ERR_INVALID_ARG). The workspace holds redmoe_balance_workspace_bytes(T, E) bytes
+ * and starts with the usual control block (zero before the first use, left zero). T == 0
+ * writes zeros forward and nothing backward. This library's own; the pages describe
+ * inference only. */
+size_t redmoe_balance_workspace_bytes(int32_t T, int32_t E);
+redmoe_status redmoe_balance_forward(const void *logits, int32_t logits_dtype, const int32_t *topk_ids,
+                                     const uint8_t *row_mask, int32_t T, int32_t E, int32_t k, float *loss,
+                                     int32_t *counts, float *prob, int32_t *n_rows, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+redmoe_status redmoe_balance_backward(const void *logits, int32_t logits_dtype, const uint8_t *row_mask, int32_t T,
+                                      int32_t E, int32_t k, const int32_t *counts, const int32_t *n_rows,
+                                      const float *grad_loss, void *dlogits, void *stream);
+
+/* ---------------------------------------------------------------------------------
+ * Matrix-vector products with one dense matrix in the expert weights' format, for the
+ * projections beside the layer: y[t, n] = sum_k x[t, k] W[n, k], T = 0..32 token rows (more:
+ * REDMOE_ERR_UNSUPPORTED). W is REDMOE_INT4G32 (others: REDMOE_ERR_UNSUPPORTED), x
+ * REDMOE_BF16 [T, cols], y REDMOE_F32 or REDMOE_BF16 [T, rows], overwritten, aligned to its
+ * element. cols is a multiple of 32 up to 65536. Products are exact and sums fp32; the order
+ * of summation is fixed for given sizes. y must not overlap x or W. */
+typedef struct redmoe_matrix {
+    int32_t rows;            /* N                                                             */
+    int32_t cols;            /* K                                                             */
+    int32_t dtype;           /* REDMOE_INT4G32                                                */
+    const void *w;           /* u8 [N, K/2], 16-byte aligned                                  */
+    const void *s;           /* bf16 [N, K/32], 16-byte aligned                               */
+} redmoe_matrix;
+redmoe_status redmoe_gemv(const redmoe_matrix *W, const void *x, int32_t x_dtype, int32_t T, void *y, int32_t y_dtype,
+                          void *stream);
+
 /* Synchronise `stream`, then read the workspace's error word: REDMOE_ERR_TIMEOUT if an
  * in-kernel grid barrier gave up waiting (bounded at about one second) since the last
  * redmoe_workspace_init; REDMOE_ERR_INVALID_ARG if a kernel found device state it cannot

@@ -9,7 +9,13 @@ redmoe_forward_stack, redmoe_forward_noalloc, redmoe_workspace_bytes,
 redmoe_workspace_init, redmoe_check_timeout, redmoe_selftest_wait_limit,
 redmoe_fill_shared_memory, redmoe_forward_cached, redmoe_expert_cache_slot_bytes,
 redmoe_expert_cache_init, redmoe_forward_host_experts, redmoe_expert_cache_prefetch,
-redmoe_status_string, redmoe_abi_version).
+redmoe_norm_forward, redmoe_norm_backward, redmoe_norm_workspace_bytes, redmoe_forward_block,
+redmoe_workspace_bytes_block, redmoe_balance_forward, redmoe_balance_backward,
+redmoe_balance_workspace_bytes, redmoe_gemv, redmoe_status_string, redmoe_abi_version).
+
+The calls around the layer (norms, block, balance, gemv) check their tensors' types, shapes,
+contiguity and device (ValueError) and run on the tensors' device, by default on that device's
+current stream.
 """
 
 from __future__ import annotations
@@ -33,7 +39,10 @@ SYMBOLS = ("redmoe_abi_version", "redmoe_status_string", "redmoe_workspace_bytes
            "redmoe_check_timeout", "redmoe_forward_noalloc", "redmoe_selftest_wait_limit",
            "redmoe_fill_shared_memory", "redmoe_forward_cached", "redmoe_expert_cache_slot_bytes",
            "redmoe_expert_cache_init", "redmoe_forward_host_experts", "redmoe_expert_cache_prefetch",
-           "redmoe_workspace_bytes_host", "redmoe_forward_host", "redmoe_forward_stack_host")
+           "redmoe_workspace_bytes_host", "redmoe_forward_host", "redmoe_forward_stack_host",
+           "redmoe_norm_forward", "redmoe_norm_workspace_bytes", "redmoe_norm_backward",
+           "redmoe_workspace_bytes_block", "redmoe_forward_block", "redmoe_balance_workspace_bytes",
+           "redmoe_balance_forward", "redmoe_balance_backward", "redmoe_gemv")
 
 _lock = threading.Lock()
 _lib = None
@@ -63,6 +72,17 @@ class _ExpertCache(C.Structure):
                 ("slot_s_gate", C.c_void_p), ("slot_s_up", C.c_void_p), ("slot_s_down", C.c_void_p),
                 ("slot_of", C.c_void_p), ("expert_in", C.c_void_p), ("hot", C.c_void_p), ("stats", C.c_void_p),
                 ("fill", C.c_void_p)]
+
+
+class _Norm(C.Structure):
+    _fields_ = [("hidden", C.c_int32), ("h_dtype", C.c_int32), ("y_dtype", C.c_int32), ("x_dtype", C.c_int32),
+                ("w_dtype", C.c_int32), ("post_norm", C.c_int32), ("gate_kind", C.c_int32), ("gate_act", C.c_int32),
+                ("gate_dtype", C.c_int32), ("eps", C.c_float), ("w_offset", C.c_float), ("res_scale", C.c_float),
+                ("block_scale", C.c_float), ("post_w", C.c_void_p), ("pre_w", C.c_void_p)]
+
+
+class _Matrix(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("cols", C.c_int32), ("dtype", C.c_int32), ("w", C.c_void_p), ("s", C.c_void_p)]
 
 
 class _RouteDebug(C.Structure):
@@ -119,6 +139,24 @@ def load():
         lib.redmoe_forward_host.argtypes = [P, P, i32, P, P, P, P, sz, P]
         lib.redmoe_forward_stack_host.restype = i32
         lib.redmoe_forward_stack_host.argtypes = [P, i32, P, i32, P, P, P, P, sz, P]
+        lib.redmoe_norm_forward.restype = i32
+        lib.redmoe_norm_forward.argtypes = [P, P, P, P, i32, P, P, P]
+        lib.redmoe_norm_workspace_bytes.restype = sz
+        lib.redmoe_norm_workspace_bytes.argtypes = [P, i32]
+        lib.redmoe_norm_backward.restype = i32
+        lib.redmoe_norm_backward.argtypes = [P, P, P, P, P, P, i32, P, P, P, P, P, P, sz, P]
+        lib.redmoe_workspace_bytes_block.restype = sz
+        lib.redmoe_workspace_bytes_block.argtypes = [P, i32]
+        lib.redmoe_forward_block.restype = i32
+        lib.redmoe_forward_block.argtypes = [P, P, P, P, P, i32, P, P, P, P, P, sz, P]
+        lib.redmoe_balance_workspace_bytes.restype = sz
+        lib.redmoe_balance_workspace_bytes.argtypes = [i32, i32]
+        lib.redmoe_balance_forward.restype = i32
+        lib.redmoe_balance_forward.argtypes = [P, i32, P, P, i32, i32, i32, P, P, P, P, P, sz, P]
+        lib.redmoe_balance_backward.restype = i32
+        lib.redmoe_balance_backward.argtypes = [P, i32, P, i32, i32, i32, P, P, P, P, P]
+        lib.redmoe_gemv.restype = i32
+        lib.redmoe_gemv.argtypes = [P, P, i32, i32, P, i32, P]
         if lib.redmoe_abi_version() != ABI_VERSION:
             raise RuntimeError("libredmoe.so ABI version mismatch")
         _lib = lib
@@ -397,3 +435,255 @@ def redmoe_expert_cache_prefetch(layer: Layer, cache: ExpertCache, ids: torch.Te
     st = load().redmoe_expert_cache_prefetch(layer.ref, cache.ref, _ptr(ids), int(ids.numel()), _ptr(workspace),
                                              workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "redmoe_expert_cache_prefetch")
+
+
+# ------------------------------------------------------------------ around the layer
+TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+_CODES = {torch.float32: 0, torch.bfloat16: 1}
+GATES = {"none": 0, "token": 1, "channel": 2, "element": 3}
+GATE_ACTS = {"linear": 0, "sigmoid": 1}
+
+
+def _arg(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: int):
+    """The address of a tensor argument, checked; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on cuda:{dev}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return dev
+
+
+def _work(workspace: Optional[torch.Tensor], dev: int):
+    """(address, bytes) of a workspace tensor or (None, 0)."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}, got one on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _call(fn, where: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) with `dev` current; the default stream is dev's current one."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    if st != 0:
+        raise RedmoeError(st, where)
+
+
+class Norm:
+    """The step between blocks (redmoe_norm): u = N(y; post_w) or y, h_out = res_scale h +
+    block_scale g u, x = N(h_out; pre_w), with N the RMS norm and g the gate.
+
+    gate: "none", "token" [T], "channel" [H] or "element" [T, H]; gate_act: "linear" or
+    "sigmoid". Weights are [H] in one dtype, or None (factor 1); post_norm defaults to whether
+    post_w is given. The weights are kept alive by this object.
+    """
+
+    def __init__(self, hidden: int, h_dtype: str = "bf16", y_dtype: str = "f32", x_dtype: str = "bf16",
+                 pre_w: Optional[torch.Tensor] = None, post_w: Optional[torch.Tensor] = None,
+                 post_norm: Optional[bool] = None, gate: str = "none", gate_act: str = "linear",
+                 gate_dtype: str = "bf16", eps: float = 1e-6, w_offset: float = 0.0, res_scale: float = 1.0,
+                 block_scale: float = 1.0):
+        if pre_w is not None and post_w is not None and pre_w.dtype is not post_w.dtype:
+            raise ValueError(f"pre_w and post_w have one dtype: got {pre_w.dtype} and {post_w.dtype}")
+        first = pre_w if pre_w is not None else post_w
+        self.device = None
+        if first is not None:
+            if first.dtype not in _CODES:
+                raise ValueError(f"norm weights are float32 or bfloat16: got {first.dtype}")
+            self.device = _device_of(first, "pre_w" if pre_w is not None else "post_w")
+        s = _Norm()
+        s.hidden = hidden
+        s.h_dtype, s.y_dtype, s.x_dtype = DTYPES[h_dtype], DTYPES[y_dtype], DTYPES[x_dtype]
+        s.w_dtype = _CODES[first.dtype] if first is not None else 0
+        s.post_norm = int(post_w is not None if post_norm is None else post_norm)
+        s.gate_kind, s.gate_act, s.gate_dtype = GATES[gate], GATE_ACTS[gate_act], DTYPES[gate_dtype]
+        s.eps, s.w_offset, s.res_scale, s.block_scale = eps, w_offset, res_scale, block_scale
+        dt = first.dtype if first is not None else None
+        s.pre_w = _arg(pre_w, "pre_w", (hidden,), dt, self.device)
+        s.post_w = _arg(post_w, "post_w", (hidden,), dt, self.device)
+        self.struct, self.ref = s, C.byref(s)
+        self.hidden, self.gate = hidden, gate
+        self.pre_w, self.post_w = pre_w, post_w
+        self.h_torch, self.y_torch, self.x_torch, self.gate_torch = (TORCH_DTYPES[d] for d in
+                                                                     (h_dtype, y_dtype, x_dtype, gate_dtype))
+
+    def gate_shape(self, T: int):
+        return {"none": (0,), "token": (T,), "channel": (self.hidden,), "element": (T, self.hidden)}[self.gate]
+
+    def _dev(self, t: torch.Tensor, name: str) -> int:
+        dev = _device_of(t, name)
+        if self.device is not None and self.device != dev:
+            raise ValueError(f"{name} is on cuda:{dev}, the norm's weights on cuda:{self.device}")
+        return dev
+
+
+def redmoe_norm_forward(norm: Norm, h: torch.Tensor, h_out: Optional[torch.Tensor] = None,
+                        x: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None, stream=None) -> None:
+    """x <- N(h) (no y), or h_out [T,H] (may be h) and, where given, x [T,H] <- the residual step on (h, y)."""
+    dev, T = norm._dev(h, "h"), h.shape[0]
+    rows = (T, norm.hidden)
+    _call(load().redmoe_norm_forward, "redmoe_norm_forward", dev, stream, norm.ref, _arg(h, "h", rows, norm.h_torch, dev),
+          _arg(y, "y", rows, norm.y_torch, dev),
+          None if gate is None else _arg(gate, "gate", norm.gate_shape(T), norm.gate_torch, dev), T,
+          _arg(h_out, "h_out", rows, norm.h_torch, dev), _arg(x, "x", rows, norm.x_torch, dev))
+
+
+def redmoe_norm_workspace_bytes(norm: Norm, T: int) -> int:
+    return int(load().redmoe_norm_workspace_bytes(norm.ref, int(T)))
+
+
+def new_norm_workspace(norm: Norm, T: int, device=None) -> torch.Tensor:
+    """A zeroed workspace tensor for redmoe_norm_backward at T rows."""
+    n = redmoe_norm_workspace_bytes(norm, T)
+    if n == 0:
+        raise ValueError("invalid norm or token count")
+    if device is None:
+        device = "cuda" if norm.device is None else f"cuda:{norm.device}"
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def redmoe_norm_backward(norm: Norm, h_out: torch.Tensor, dh: torch.Tensor, workspace: Optional[torch.Tensor],
+                         dh_out: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                         y: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                         dy: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                         dpost_w: Optional[torch.Tensor] = None, dpre_w: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """dh, dy, dgate, dpost_w and dpre_w (fp32 [H]) <- the gradients dh_out and dx that arrive at
+    h_out and x. dgate is fp32 for a token or channel gate, the gate's dtype for an element gate."""
+    dev, T = norm._dev(h_out, "h_out"), h_out.shape[0]
+    rows, cols, f32 = (T, norm.hidden), (norm.hidden,), torch.float32
+    g = dg = None
+    if gate is not None:
+        g = _arg(gate, "gate", norm.gate_shape(T), norm.gate_torch, dev)
+    if dgate is not None:
+        dg = _arg(dgate, "dgate", norm.gate_shape(T), norm.gate_torch if norm.gate == "element" else f32, dev)
+    ws, nbytes = _work(workspace, dev)
+    _call(load().redmoe_norm_backward, "redmoe_norm_backward", dev, stream, norm.ref,
+          _arg(h_out, "h_out", rows, norm.h_torch, dev), _arg(y, "y", rows, norm.y_torch, dev), g,
+          _arg(dh_out, "dh_out", rows, norm.h_torch, dev), _arg(dx, "dx", rows, norm.x_torch, dev), T,
+          _arg(dh, "dh", rows, norm.h_torch, dev), _arg(dy, "dy", rows, norm.y_torch, dev), dg,
+          _arg(dpost_w, "dpost_w", cols, f32, dev), _arg(dpre_w, "dpre_w", cols, f32, dev), ws, nbytes)
+
+
+def redmoe_workspace_bytes_block(layer: Layer, T: int) -> int:
+    return int(load().redmoe_workspace_bytes_block(layer.ref, int(T)))
+
+
+def new_workspace_block(layer: Layer, T: int, device=None) -> torch.Tensor:
+    """A zeroed workspace tensor of redmoe_workspace_bytes_block(layer, T) bytes."""
+    n = redmoe_workspace_bytes_block(layer, T)
+    if n == 0:
+        raise ValueError("invalid layer or token count")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def redmoe_forward_block(layer: Layer, before: Norm, after: Norm, h: torch.Tensor, h_out: torch.Tensor,
+                         topk_ids: torch.Tensor, topk_w: torch.Tensor, workspace: torch.Tensor,
+                         x_next: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """The residual block around the layer: x = N(h) by `before`, y = layer(x), then `after`'s step on
+    (h, y) into h_out (may be h) and, where given, x_next."""
+    dev, T = before._dev(h, "h"), h.shape[0]
+    after._dev(h, "h")
+    rows, picks = (T, layer.hidden), (T, layer.top_k)
+    ws, nbytes = _work(workspace, dev)
+    _call(load().redmoe_forward_block, "redmoe_forward_block", dev, stream, layer.ref, before.ref, after.ref,
+          _arg(h, "h", rows, before.h_torch, dev),
+          None if gate is None else _arg(gate, "gate", after.gate_shape(T), after.gate_torch, dev), T,
+          _arg(h_out, "h_out", rows, after.h_torch, dev), _arg(x_next, "x_next", rows, after.x_torch, dev),
+          _arg(topk_ids, "topk_ids", picks, torch.int32, dev), _arg(topk_w, "topk_w", picks, torch.float32, dev),
+          ws, nbytes)
+
+
+def redmoe_balance_workspace_bytes(T: int, n_experts: int) -> int:
+    return int(load().redmoe_balance_workspace_bytes(int(T), int(n_experts)))
+
+
+def new_balance_workspace(T: int, n_experts: int, device=None) -> torch.Tensor:
+    """A zeroed workspace tensor for redmoe_balance_forward."""
+    n = redmoe_balance_workspace_bytes(T, n_experts)
+    if n == 0:
+        raise ValueError("invalid token or expert count")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _logits(logits: torch.Tensor):
+    dev = _device_of(logits, "logits")
+    code = _CODES.get(logits.dtype)
+    if code is None or logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError(f"logits: expected a contiguous float32 or bfloat16 [T, E] tensor, got {logits.dtype} "
+                         f"{list(logits.shape)}")
+    return dev, code, logits.shape[0], logits.shape[1]
+
+
+def _mask(mask: Optional[torch.Tensor], T: int, dev: int):
+    if mask is not None and mask.dtype is torch.bool:
+        return _arg(mask, "mask", (T,), torch.bool, dev)
+    return _arg(mask, "mask", (T,), torch.uint8, dev)
+
+
+def redmoe_balance_forward(logits: torch.Tensor, topk_ids: torch.Tensor, loss: torch.Tensor, counts: torch.Tensor,
+                           prob: torch.Tensor, n_rows: torch.Tensor, workspace: torch.Tensor,
+                           mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """loss[2] fp32 (balance, z), counts[E] int32, prob[E] fp32, n_rows[1] int32 <- the rows of logits
+    [T,E] and topk_ids [T,k] int32 whose mask byte [T] (uint8 or bool) is not zero."""
+    dev, code, T, E = _logits(logits)
+    if topk_ids.dim() != 2:
+        raise ValueError(f"topk_ids: expected [T, k], got {list(topk_ids.shape)}")
+    k = topk_ids.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    ws, nbytes = _work(workspace, dev)
+    _call(load().redmoe_balance_forward, "redmoe_balance_forward", dev, stream, logits.data_ptr(), code,
+          _arg(topk_ids, "topk_ids", (T, k), i32, dev), _mask(mask, T, dev), T, E, k, _arg(loss, "loss", (2,), f32, dev),
+          _arg(counts, "counts", (E,), i32, dev), _arg(prob, "prob", (E,), f32, dev),
+          _arg(n_rows, "n_rows", (1,), i32, dev), ws, nbytes)
+
+
+def redmoe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, n_rows: torch.Tensor, grad_loss: torch.Tensor,
+                            dlogits: torch.Tensor, top_k: int, mask: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """dlogits [T,E] (the logits' dtype; may be logits) <- grad_loss[2] fp32, with the forward call's
+    counts, n_rows and mask."""
+    dev, code, T, E = _logits(logits)
+    _call(load().redmoe_balance_backward, "redmoe_balance_backward", dev, stream, logits.data_ptr(), code,
+          _mask(mask, T, dev), T, E, top_k, _arg(counts, "counts", (E,), torch.int32, dev),
+          _arg(n_rows, "n_rows", (1,), torch.int32, dev), _arg(grad_loss, "grad_loss", (2,), torch.float32, dev),
+          _arg(dlogits, "dlogits", (T, E), logits.dtype, dev))
+
+
+class Matrix:
+    """A dense matrix [rows, cols] in an expert weight format (redmoe_matrix): packed bytes w [rows, cols/2]
+    and bf16 scales s [rows, cols/32], kept alive by this object."""
+
+    def __init__(self, w: torch.Tensor, s: torch.Tensor, rows: int, cols: int, dtype: str = "int4g32"):
+        if dtype == "int4g32":  # other formats are refused by the call
+            dev = _device_of(w, "w")
+            _arg(w, "w", (rows, cols // 2), torch.uint8, dev)
+            _arg(s, "s", (rows, cols // 32), torch.bfloat16, dev)
+        st = _Matrix()
+        st.rows, st.cols, st.dtype, st.w, st.s = rows, cols, DTYPES[dtype], _ptr(w), _ptr(s)
+        self.struct, self.ref = st, C.byref(st)
+        self.rows, self.cols, self.w, self.s = rows, cols, w, s
+
+
+def redmoe_gemv(matrix: Matrix, x: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """y[T, rows] (fp32 or bf16) <- x[T, cols] bf16 times the matrix's transpose, T = 0..32."""
+    dev = _device_of(matrix.w, "w")
+    T = x.shape[0]
+    if x.dtype not in _CODES or y.dtype not in _CODES:
+        raise ValueError(f"x and y are float32 or bfloat16: got {x.dtype} and {y.dtype}")
+    _call(load().redmoe_gemv, "redmoe_gemv", dev, stream, matrix.ref, _arg(x, "x", (T, matrix.cols), x.dtype, dev),
+          _CODES[x.dtype], T, _arg(y, "y", (T, matrix.rows), y.dtype, dev), _CODES[y.dtype])

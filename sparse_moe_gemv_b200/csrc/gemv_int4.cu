@@ -4,27 +4,37 @@
 // What bounds it is reading W (0.5625 bytes a weight): at the copy bandwidth of a B200 that is
 // 11.7 T weights a second, 41 a clock and SM, so a weight may cost about three lane operations.
 // Multiply-adds on the CUDA cores alone would spend one per weight and token beside the
-// decoding; here the products go to the tensor cores (mma m16n8k16, bf16 operands, fp32 sums):
+// decoding; here the products go to the tensor cores (mma m16n8k16, bf16 operands, fp32 sums)
+// and a nibble is decoded by one AND:
 //
-//   A  16 rows of W as bf16 nibble - 8, exact: nibbles i and i + 4 of a word, or'ed into the
-//      mantissas of the bf16 pair (128, 128), are 128 + nibble; subtracting 136 leaves the code.
-//   B  x in the matching order of k (any order will do as long as both operands have it).
-//   C  the sums of one scale group, multiplied by its scale and added in fp32: the scale never
-//      touches an operand, so nothing is rounded before the sums.
+//   A  16 rows of W. The bf16 bit patterns 0 .. 255 are the numbers 0 .. 255 times 2^-133 (the
+//      subnormals and the first binade share their step, and mma takes both as they are), so a
+//      word's nibbles under the masks 0x000F000F and 0x00F000F0, and those of the word shifted by
+//      eight, already are pairs of bf16 numbers nibble 2^-133 and 16 nibble 2^-133.
+//   B  x in the matching order of k (any order will do as long as both operands have it), every
+//      second pair divided by 16, scaled by a power of two per token that puts its largest
+//      element just under the largest bf16: products come out near one. All of that is exact.
+//   C  starts at -8 times the group's sum of x and takes the products: the sum over a scale group
+//      of x (nibble - 8). It is multiplied by the group's scale and added up in fp32; the scale
+//      never touches an operand.
 //
-// A lane reads 16-byte chunks, one whole group of one row; the quad of lanes that shares a row
-// reads four consecutive groups. An mma sums over its quad, so it must not mix groups:
+// Products are exact (down to 2^-116 of a row's largest x). The sums of a group run over nibbles
+// of 0 .. 15, so their rounding is in proportion to 16 scale sum |x|, about three times what sums
+// of the codes -8 .. 7 would have. An infinite x makes its row NaN (infinity - infinity).
 //
-//   few rows (x has 1 or 2): the quad's four groups stay apart in the columns of B. Column
-//      4 token + group holds x for the lane of that group and zero for the other three: eight
-//      products make the sums of four groups and two tokens.
-//   more rows: the quad transposes its 4 x 4 words, after which a lane holds its quarter of each
-//      group in turn, and the eight columns of B are eight tokens.
+// An mma sums over the quad of lanes that shares its rows, so the quad must not mix groups:
 //
-// A step is 16 rows of W (a tile) by 128 columns. A block has a run of whole tiles, its warps
+//   one or two rows of x: the eight columns of B are eight groups. A lane holds one whole group
+//      (16 bytes) of one row; column j of B is x in the lane slots of group j and zero in the
+//      others, so one chain of eight products makes eight groups' sums of eight W rows.
+//   more rows: the eight columns of B are eight tokens, and a lane holds its quarter (4 bytes) of
+//      one group after the other.
+//
+// A step is 16 rows of W (a tile) by 256 columns. A block has a run of whole tiles, its warps
 // equal shares of that run's steps; a tile whose steps fall to several warps is added up through
-// shared memory in warp order, so results do not depend on timing. Loads run two steps ahead
-// in registers.
+// shared memory in warp order, so results do not depend on timing. Each warp copies its steps
+// into a ring of its own with asynchronous copies (128-byte lines asked for whole), so no warp
+// waits for another until the end, and the loads in flight need no registers.
 #include "common.cuh"
 #include "internal.h"
 
@@ -33,12 +43,17 @@
 namespace redmoe {
 namespace {
 
+constexpr int GV_WARPS = 16;
 constexpr int GV_MAX_T = 32;
-constexpr int GV_STEP = 128;     // columns of a step: four groups
 constexpr int GV_MAX_K = 65536;
-constexpr int GV_PAD = 64;       // bytes between token rows in shared memory (bank offset)
-constexpr int GV_AHEAD = 2;      // steps of a load batch; one batch is in flight while one is used
-constexpr int GV_ZERO = 256;     // bytes of zeros: one step of an absent token
+constexpr int GV_COLS = 256;     // columns of a step
+constexpr int GV_PAD = 64;       // bytes between token rows of x in shared memory (bank offset)
+constexpr int GV_ZERO = 256;     // bytes of zeros: half a step of an absent token
+constexpr int GV_WROW = GV_COLS / 2 + 16;                  // bytes of a slot's row of W (bank offset)
+constexpr int GV_SROW = GV_COLS / 16;                      // bytes of a slot's row of scales
+constexpr int GV_SLOT = 16 * (GV_WROW + GV_SROW);
+constexpr int GV_SLOTS = 4;      // of a warp's ring: three steps in flight while one is used
+constexpr int GV_RING = GV_SLOTS * GV_SLOT;
 
 struct GemvParams {
     const uint8_t* w;      // [N, K/2]
@@ -48,48 +63,214 @@ struct GemvParams {
     int N, K, T;
 };
 
-__device__ __forceinline__ uint32_t dequant2(uint32_t w) {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(v) : "r"(w));  // (w & a) | b
-    const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
-    return *reinterpret_cast<const uint32_t*>(&d);
+__host__ __device__ __forceinline__ int row_stride(int K) { return (K + GV_COLS - 1) / GV_COLS * (2 * GV_COLS) + GV_PAD; }
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// d = c0 c1 in both rows + the products of one word of two rows with eight columns of x.
+__device__ __forceinline__ void mma_word(float (&d)[4], uint32_t a, uint32_t b, const uint4& x, float c0, float c1,
+                                         float c2, float c3) {
+    constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
+    mma_bf16(d, a & LO, b & LO, a & HI, b & HI, x.x, x.y, c0, c1, c2, c3);
+    mma_bf16(d, (a >> 8) & LO, (b >> 8) & LO, (a >> 8) & HI, (b >> 8) & HI, x.z, x.w, d[0], d[1], d[2], d[3]);
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
-// Copy x's T rows to shared memory, every run of eight columns in the order (0,4) (1,5) (2,6)
-// (3,7) in which dequant2 yields a word's nibbles; zeros beyond K, and a step of zeros behind.
-template <int THREADS>
-__device__ __forceinline__ void stage_x(const GemvParams& p, int steps, int stride, unsigned char* xs) {
-    const int runs = steps * (GV_STEP / 8);
-    for (int i = threadIdx.x; i < p.T * runs; i += THREADS) {
+// The exponent that a row's largest x is scaled to: the largest with room for rounding sums.
+constexpr int GV_TOP = 126;
+
+// x's T rows in shared memory as B wants them: every run of eight columns in the order (0,4)
+// (1,5)/16 (2,6) (3,7)/16, times 2^(GV_TOP - e) with e the exponent of the row's largest finite
+// element; zeros beyond K, and GV_ZERO of them behind. gsum: -8 times the sum of each group, in
+// the units of the products (FEW: [token][group], else [group][token]). exps[t] = e.
+template <bool FEW, int TOK>
+__device__ __forceinline__ void stage_x(const GemvParams& p, int stride, unsigned char* xs, float* gsum, int* exps) {
+    const int runs = (stride - GV_PAD) / 16;  // a multiple of 32: a warp's lanes are in one row
+    for (int i = threadIdx.x; i < TOK; i += blockDim.x) exps[i] = 0;
+    if (threadIdx.x < GV_ZERO / 16)
+        *reinterpret_cast<uint4*>(xs + size_t(p.T) * stride + 16 * threadIdx.x) = make_uint4(0u, 0u, 0u, 0u);
+    if (!FEW) {  // absent tokens
+        for (int i = threadIdx.x; i < runs / 4 * TOK; i += blockDim.x)
+            if (i % TOK >= p.T) gsum[i] = 0.0f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T * runs; i += blockDim.x) {
         const int t = i / runs, r = i - t * runs;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (8 * r < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + size_t(t) * p.K + 8 * r));
-        *reinterpret_cast<uint4*>(xs + size_t(t) * stride + 16 * r) =
-            make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                       __byte_perm(v.y, v.w, 0x7632));
+        *reinterpret_cast<uint4*>(xs + size_t(t) * stride + 16 * r) = v;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0;  // largest magnitude as a bit pattern; infinities and NaN do not count
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+            if (lo < 0x7f80u) top = max(top, lo);
+            if (hi < 0x7f80u) top = max(top, hi);
+        }
+        top = __reduce_max_sync(FULL, top);
+        if ((threadIdx.x & 31) == 0) atomicMax(&exps[t], int(top));
     }
-    if (threadIdx.x < GV_ZERO / 16)
-        *reinterpret_cast<uint4*>(xs + size_t(p.T) * stride + 16 * threadIdx.x) = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T * runs; i += blockDim.x) {
+        const int t = i / runs, r = i - t * runs;
+        // the scale 2^(GV_TOP - e) as two factors: e is -126 .. 127 (rows of subnormals: -126)
+        const int e = max(exps[t] >> 7, 1) - 127, up = GV_TOP - e;
+        const float f0 = __int_as_float((127 + up / 2) << 23), f1 = __int_as_float((127 + up - up / 2) << 23);
+        const uint4 v = *reinterpret_cast<const uint4*>(xs + size_t(t) * stride + 16 * r);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float f[8], s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = bf16lo(w[j]) * f0 * f1;
+            f[2 * j + 1] = bf16hi(w[j]) * f0 * f1;
+            s += f[2 * j] * 0x1p-64f + f[2 * j + 1] * 0x1p-64f;
+        }
+        s += __shfl_xor_sync(FULL, s, 1);
+        s += __shfl_xor_sync(FULL, s, 2);
+        const float k = 0.0625f;
+        auto pair = [](float lo, float hi) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+            return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        *reinterpret_cast<uint4*>(xs + size_t(t) * stride + 16 * r) =
+            make_uint4(pair(f[0], f[4]), pair(f[1] * k, f[5] * k), pair(f[2], f[6]), pair(f[3] * k, f[7] * k));
+        if ((r & 3) == 0) gsum[FEW ? t * (runs / 4) + r / 4 : (r / 4) * TOK + t] = s * -0x1p-66f;  // -8 2^(64 - 133)
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T; i += blockDim.x) exps[i] = max(exps[i] >> 7, 1) - 127;
+    __syncthreads();
 }
 
-// The 4 x 4 words of a quad, transposed: lane t ends with word t of the four lanes' chunks.
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
-    const bool odd = t & 1, high = t & 2;
-    {
-        const uint32_t a = __shfl_xor_sync(FULL, odd ? w[0] : w[1], 1), b = __shfl_xor_sync(FULL, odd ? w[2] : w[3], 1);
-        if (odd) { w[0] = a; w[2] = b; } else { w[1] = a; w[3] = b; }
+// Position in a warp's share of steps, with the lane's first address there: eight lanes read 128
+// bytes of a row, lane l chunk l % 8 of rows l / 8 + 4 j.
+struct Cursor {
+    const uint8_t* w;
+    const uint16_t* sc;  // scales of row lane % 16
+    int tile, s;
+    __device__ __forceinline__ void at(const GemvParams& p, int tile_, int s_, int lane) {
+        tile = tile_;
+        s = s_;
+        w = p.w + size_t(tile * 16 + lane / 8) * (p.K / 2) + size_t(s) * (GV_COLS / 2) + 16 * (lane % 8);
+        sc = p.s + size_t(tile * 16 + lane % 16) * (p.K / 32) + s * (GV_COLS / 32);
     }
-    {
-        const uint32_t a = __shfl_xor_sync(FULL, high ? w[0] : w[2], 2), b = __shfl_xor_sync(FULL, high ? w[1] : w[3], 2);
-        if (high) { w[0] = a; w[1] = b; } else { w[2] = a; w[3] = b; }
+    __device__ __forceinline__ void next(const GemvParams& p, int steps, int lane) {
+        w += GV_COLS / 2;
+        sc += GV_COLS / 32;
+        if (++s == steps) at(p, tile + 1, 0, lane);
+    }
+};
+
+// Ask for one step. Rows beyond N and columns beyond K keep what the slot holds: any code is
+// finite and meets a zero x or an output that is not stored. Scales beyond K are zeroed (what
+// lies there need not be finite). WHOLE: K % 256 == 0, a row's scales of a step are 16 bytes.
+template <bool WHOLE>
+__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor& c, int lane, unsigned char* slot) {
+    const uint32_t dst = smem_u32(slot) + (lane / 8) * GV_WROW + 16 * (lane % 8);
+    const int groups = p.K / 32 - c.s * (GV_COLS / 32);  // groups left in the row
+    const size_t step4 = size_t(p.K) * 2;  // bytes of four rows
+    if (WHOLE || lane % 8 < groups) {
+        if (c.tile * 16 + 16 <= p.N) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c.tile * 16 + lane / 8 + 4 * j < p.N) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
+        }
+    }
+    unsigned char* ss = slot + 16 * GV_WROW + (lane % 16) * GV_SROW;
+    if (c.tile * 16 + lane % 16 < p.N) {
+        if (WHOLE) {
+            if (lane < 16) cp_async16(smem_u32(ss), c.sc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = 4 * (lane / 16) + i;
+                reinterpret_cast<uint16_t*>(ss)[k] = k < groups ? __ldg(c.sc + k) : uint16_t(0);
+            }
+        }
+    }
+}
+
+// One or two tokens, 16 rows by 256 columns: lane (g, q) reads chunk q + 4 (g & 1) of rows
+// g / 2 + 4 j. The rows g of an mma are a W row's first four groups (g even) and its last four
+// (g odd): columns 2 q, 2 q + 1 of a lane's sums count where they are that half's.
+// w: the lane's first chunk, s: the first row's scales, x: the lane's column of B (zeros in the
+// lanes that hold other groups), xrow bytes from one token's to the next.
+// gs: this lane's pair of group sums, grow floats from one token's to the next.
+template <int TOK>
+__device__ __forceinline__ void few_step(const unsigned char* w, const unsigned char* s, const unsigned char* x, int xrow,
+                                         const float* gs, int grow, float (&acc)[4 * TOK]) {
+    float cc[TOK][2][4];
+    uint4 v[4];
+    uint32_t sc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * GV_WROW);
+        sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * GV_SROW);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(x + t * xrow + 16 * i);
+            const float2 c = i == 0 ? *reinterpret_cast<const float2*>(gs + t * grow) : make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 va = v[2 * h], vb = v[2 * h + 1];
+                const uint32_t a = i == 0 ? va.x : i == 1 ? va.y : i == 2 ? va.z : va.w;
+                const uint32_t b = i == 0 ? vb.x : i == 1 ? vb.y : i == 2 ? vb.z : vb.w;
+                float(&d)[4] = cc[t][h];
+                if (i == 0) mma_word(d, a, b, xv, c.x, c.y, c.x, c.y);
+                else mma_word(d, a, b, xv, d[0], d[1], d[2], d[3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float s0 = bf16lo(sc[j]), s1 = bf16hi(sc[j]);
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            const int k = 4 * t + j, c = 2 * (j & 1);
+            acc[k] = fmaf(cc[t][j / 2][c], s0, fmaf(cc[t][j / 2][c + 1], s1, acc[k]));
+        }
+    }
+}
+
+// Eight NT tokens, 16 rows by 128 columns: lane (g, q) reads its quarter of the four groups of
+// rows g and g + 8; x holds the lane's token of each block of eight, gs the group sums of the
+// lane's two tokens of C in the first block.
+template <int NT>
+__device__ __forceinline__ void row_step(const unsigned char* w, const unsigned char* s, const unsigned char* const (&x)[NT],
+                                         const float* gs, float (&acc)[4 * NT]) {
+    const uint2 sa = *reinterpret_cast<const uint2*>(s), sb = *reinterpret_cast<const uint2*>(s + 8 * GV_SROW);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(w + 16 * i);
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(w + 8 * GV_WROW + 16 * i);
+        const uint32_t ua = i < 2 ? sa.x : sa.y, ub = i < 2 ? sb.x : sb.y;
+        const float fa = i & 1 ? bf16hi(ua) : bf16lo(ua), fb = i & 1 ? bf16hi(ub) : bf16lo(ub);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x[nt] + 64 * i);
+            const float2 c = *reinterpret_cast<const float2*>(gs + i * (8 * NT) + 8 * nt);
+            float cc[4];
+            mma_word(cc, a, b, v, c.x, c.y, c.x, c.y);
+            acc[4 * nt + 0] = fmaf(cc[0], fa, acc[4 * nt + 0]);
+            acc[4 * nt + 1] = fmaf(cc[1], fa, acc[4 * nt + 1]);
+            acc[4 * nt + 2] = fmaf(cc[2], fb, acc[4 * nt + 2]);
+            acc[4 * nt + 3] = fmaf(cc[3], fb, acc[4 * nt + 3]);
+        }
     }
 }
 
@@ -99,231 +280,134 @@ __device__ __forceinline__ void put(void* y, size_t i, float v) {
     else static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
 }
 
-// One step's operands as they come from memory: this lane's group of rows r0 and r1 and the
-// scales that its sums need.
-template <int NT>
-struct Step {
-    static constexpr int NS = NT ? 4 : 2;
-    uint32_t a[4], b[4], s[NS];
-};
-
-// Position in a run of steps: 128 columns `s` of tile `tile`, with the lane's addresses there.
-struct Cursor {
-    const uint8_t *w0, *w1;
-    const uint16_t *s0, *s1;
-    int tile, s;
-    __device__ __forceinline__ void at(const GemvParams& p, int tile_, int s_, int g, int q) {
-        tile = tile_;
-        s = s_;
-        const int r0 = min(tile * 16 + g, p.N - 1), r1 = min(tile * 16 + g + 8, p.N - 1);
-        w0 = p.w + size_t(r0) * (p.K / 2) + size_t(s) * 64 + 16 * q;
-        w1 = p.w + size_t(r1) * (p.K / 2) + size_t(s) * 64 + 16 * q;
-        s0 = p.s + size_t(r0) * (p.K / 32) + 4 * s;
-        s1 = p.s + size_t(r1) * (p.K / 32) + 4 * s;
-    }
-    __device__ __forceinline__ void next(const GemvParams& p, int steps, int g, int q) {
-        if (++s == steps) {
-            at(p, tile + 1, 0, g, q);
-            return;
-        }
-        w0 += 64;
-        w1 += 64;
-        s0 += 4;
-        s1 += 4;
-    }
-};
-
-// A pair of bf16 scales; ALIGNED: K % 128 == 0, every step has four groups and starts on 8 bytes.
-__device__ __forceinline__ uint32_t scale2(const uint16_t* s, int i, int left) {
-    const uint32_t lo = i < left ? __ldg(s + i) : 0, hi = i + 1 < left ? __ldg(s + i + 1) : 0;
-    return lo | (hi << 16);
-}
-
-template <int NT, bool ALIGNED>
-__device__ __forceinline__ void load_step(const GemvParams& p, const Cursor& c, int q, Step<NT>& st) {
-    const int left = p.K / 32 - 4 * c.s;  // groups from this step's first to the row's end
-    uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
-    if (ALIGNED || q < left) {
-        u = ld_stream(c.w0);
-        v = ld_stream(c.w1);
-    }
-    st.a[0] = u.x; st.a[1] = u.y; st.a[2] = u.z; st.a[3] = u.w;
-    st.b[0] = v.x; st.b[1] = v.y; st.b[2] = v.z; st.b[3] = v.w;
-    if (NT == 0) {  // this lane's two columns: groups 2 (q & 1) and 2 (q & 1) + 1
-        const int i = 2 * (q & 1);
-        st.s[0] = ALIGNED ? __ldg(reinterpret_cast<const uint32_t*>(c.s0 + i)) : scale2(c.s0, i, left);
-        st.s[1] = ALIGNED ? __ldg(reinterpret_cast<const uint32_t*>(c.s1 + i)) : scale2(c.s1, i, left);
-    } else if (ALIGNED) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(c.s0)), y = __ldg(reinterpret_cast<const uint2*>(c.s1));
-        st.s[0] = x.x; st.s[1] = x.y; st.s[2 % Step<NT>::NS] = y.x; st.s[3 % Step<NT>::NS] = y.y;
-    } else {
-        st.s[0] = scale2(c.s0, 0, left);
-        st.s[1] = scale2(c.s0, 2, left);
-        st.s[2 % Step<NT>::NS] = scale2(c.s1, 0, left);
-        st.s[3 % Step<NT>::NS] = scale2(c.s1, 2, left);
-    }
-}
-
-// acc += the step's products. xp: this lane's x at the step's first column, of its token and
-// group (few rows) or of each of its NT tokens.
-__device__ __forceinline__ void few_step(const Step<0>& st, const unsigned char* xp, float (&acc)[2]) {
-    float cc[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint4 x = reinterpret_cast<const uint4*>(xp)[i];
-        const uint32_t a = st.a[i], b = st.b[i];
-        mma_bf16(cc, dequant2(a), dequant2(b), dequant2(a >> 4), dequant2(b >> 4), x.x, x.y);
-        mma_bf16(cc, dequant2(a >> 8), dequant2(b >> 8), dequant2(a >> 12), dequant2(b >> 12), x.z, x.w);
-    }
-    acc[0] = fmaf(cc[0], bf16lo(st.s[0]), fmaf(cc[1], bf16hi(st.s[0]), acc[0]));
-    acc[1] = fmaf(cc[2], bf16lo(st.s[1]), fmaf(cc[3], bf16hi(st.s[1]), acc[1]));
-}
-
-template <int NT>
-__device__ __forceinline__ void row_step(Step<NT>& st, const unsigned char* const (&xp)[NT], int q, float (&acc)[4 * NT]) {
-    quad_transpose(st.a, q);
-    quad_transpose(st.b, q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float sa = i & 1 ? bf16hi(st.s[i / 2]) : bf16lo(st.s[i / 2]);
-        const float sb = i & 1 ? bf16hi(st.s[2 + i / 2]) : bf16lo(st.s[2 + i / 2]);
-        const uint32_t a = st.a[i], b = st.b[i];
-        const uint32_t a0 = dequant2(a), a1 = dequant2(b), a2 = dequant2(a >> 4), a3 = dequant2(b >> 4),
-                       a4 = dequant2(a >> 8), a5 = dequant2(b >> 8), a6 = dequant2(a >> 12), a7 = dequant2(b >> 12);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint4 x = *reinterpret_cast<const uint4*>(xp[nt] + 64 * i);
-            float cc[4] = {};
-            mma_bf16(cc, a0, a1, a2, a3, x.x, x.y);
-            mma_bf16(cc, a4, a5, a6, a7, x.z, x.w);
-            acc[4 * nt + 0] = fmaf(cc[0], sa, acc[4 * nt + 0]);
-            acc[4 * nt + 1] = fmaf(cc[1], sa, acc[4 * nt + 1]);
-            acc[4 * nt + 2] = fmaf(cc[2], sb, acc[4 * nt + 2]);
-            acc[4 * nt + 3] = fmaf(cc[3], sb, acc[4 * nt + 3]);
-        }
-    }
-}
-
-// Results of one tile: NT = 0 after adding the two lanes of a token.
-template <int NT, bool F32, int NA>
-__device__ __forceinline__ void put_tile(const GemvParams& p, int tile, int g, int q, const float (&acc)[NA]) {
-    const int n0 = tile * 16 + g, n1 = n0 + 8;
-    if (NT == 0) {
-        const int t = q >> 1;
-        if ((q & 1) == 0 && t < p.T) {
-            if (n0 < p.N) put<F32>(p.y, size_t(t) * p.N + n0, acc[0]);
-            if (n1 < p.N) put<F32>(p.y, size_t(t) * p.N + n1, acc[1]);
-        }
-    } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = nt * 8 + 2 * q + (i & 1), n = i < 2 ? n0 : n1;
-                if (t < p.T && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, acc[(4 * nt + i) % NA]);
-            }
-        }
-    }
-}
-
-// NT = 0: one or two tokens; otherwise NT blocks of eight tokens. All of x in shared memory.
-template <int NT, bool F32, bool ALIGNED, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) gemv_kernel(const GemvParams p) {
+// NT < 0: -NT tokens (one or two); otherwise NT blocks of eight. All of x in shared memory.
+template <int NT, bool F32, bool WHOLE>
+__global__ void __launch_bounds__(32 * GV_WARPS, 1) gemv_kernel(const GemvParams p) {
     extern __shared__ __align__(16) unsigned char sm[];
-    constexpr int NA = NT ? 4 * NT : 2;   // sums a lane holds
-    const int steps = (p.K + GV_STEP - 1) / GV_STEP;
-    const int stride = steps * (2 * GV_STEP) + GV_PAD;
-    unsigned char* xs = sm;
-    unsigned char* zero = xs + size_t(p.T) * stride;  // x of absent tokens and of other groups
-    float* red = reinterpret_cast<float*>(zero + GV_ZERO);  // [WARPS][NA][32]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr bool FEW = NT <= 0;
+    constexpr int TOK = FEW ? -NT : 8 * NT;
+    constexpr int NA = FEW ? 4 * TOK : 4 * NT;  // sums a lane holds
+    const int steps = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int g = lane >> 2, q = lane & 3;
+    unsigned char* xs = sm;
+    unsigned char* zero = xs + size_t(p.T) * stride;
+    int* exps = reinterpret_cast<int*>(zero + GV_ZERO);     // [TOK], in 128 bytes
+    float* gsum = reinterpret_cast<float*>(exps + 32);      // [TOK][8 steps] or [8 steps][TOK]
+    float* red = gsum + TOK * 8 * steps;                    // [warps][NA][32]
+    unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * GV_RING;
+
     const int ntiles = (p.N + 15) / 16;
     const int ta = int((long long)ntiles * blockIdx.x / gridDim.x), tb = int((long long)ntiles * (blockIdx.x + 1) / gridDim.x);
-    // at most 2^24 tiles over 148 blocks or more, of 512 steps: total * WARPS < 2^30
+    // at most 2^24 tiles over 148 blocks or more, of 256 steps: total * warps < 2^30
     const int total = (tb - ta) * steps;
-    auto begin = [&](int w) { return total * w / WARPS; };
+    auto begin = [&](int w) { return total * w / warps; };
     const int za = begin(warp), zb = begin(warp + 1);
 
     Cursor in;
-    in.at(p, ta + za / steps, za % steps, g, q);
-    int tile = in.tile, s = in.s;
-    int zin = za;
-    Step<NT> st[2][GV_AHEAD];
-    auto fetch = [&](Step<NT> (&to)[GV_AHEAD]) {
-#pragma unroll
-        for (int i = 0; i < GV_AHEAD; ++i) {
-            if (zin < zb) {
-                load_step<NT, ALIGNED>(p, in, q, to[i]);
-                in.next(p, steps, g, q);
-            }
+    in.at(p, ta + za / steps, za % steps, lane);
+    int tile = in.tile, s = in.s, zin = za, sin = 0;
+    auto ask = [&]() {  // one group per call, an empty one behind the last step
+        if (zin < zb) {
+            fetch<WHOLE>(p, in, lane, ring + sin);
+            in.next(p, steps, lane);
+            sin = sin + GV_SLOT == GV_RING ? 0 : sin + GV_SLOT;
             ++zin;
         }
+        cp_commit();
     };
-    fetch(st[0]);
-    stage_x<32 * WARPS>(p, steps, stride, xs);
-    __syncthreads();
+    #pragma unroll
+    for (int i = 0; i < GV_SLOTS - 1; ++i) ask();
+    stage_x<FEW, TOK>(p, stride, xs, gsum, exps);
 
-    constexpr int NX = NT ? NT : 1;
-    const unsigned char* x0[NX];  // this lane's x in step 0, and what a step adds
-    int xstep[NX];
+    const int xrow = FEW && (g & 3) == q ? stride : 0;
+    constexpr int NX = FEW ? 1 : NT;
+    const unsigned char* x0[NX];
+    int xstep[NX];  // bytes a step adds
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-        const int t = NT ? 8 * i + g : g >> 2;
-        const bool mine = t < p.T && (NT || (g & 3) == q);
-        x0[i] = (mine ? xs + size_t(t) * stride : zero) + (NT ? 16 * q : (mine ? 64 * q : 0));
-        xstep[i] = mine ? 2 * GV_STEP : 0;
+        const bool there = FEW ? (g & 3) == q : 8 * i + g < p.T;  // few tokens: this lane is its column's group
+        x0[i] = (there ? xs + (FEW ? 64 * g : (8 * i + g) * stride) : zero) + (FEW ? 0 : 16 * q);
+        xstep[i] = there ? 2 * GV_COLS : 0;
     }
+    const unsigned char* my_w = ring + (FEW ? (lane / 8) * GV_WROW + 16 * (lane % 8) : g * GV_WROW + 4 * q);
+    const unsigned char* my_s = ring + 16 * GV_WROW + (FEW ? (lane / 8) * GV_SROW + 4 * q : g * GV_SROW);
+    const float* my_g = gsum + 2 * q;
+
     float acc[NA] = {};
-    bool whole = s == 0;  // the segment at hand starts at its tile's first step
-    auto finish = [&](bool last) {  // the segment ends: behind its tile's last step, or (last) before it
-        if (NT == 0) {
-            acc[0] += __shfl_xor_sync(FULL, acc[0], 1);
-            acc[1] += __shfl_xor_sync(FULL, acc[1], 1);
+    auto put_tile = [&](int tl, const float (&v)[NA]) {
+        if constexpr (FEW) {
+            const int m = lane % 8;  // the sums are in all eight lanes of a row: lane m stores sum m
+            float u = v[0];
+#pragma unroll
+            for (int i = 1; i < NA; ++i) u = m == i ? v[i] : u;
+            const int n = tl * 16 + lane / 8 + 4 * (m & 3), t = m >> 2;
+            if (m < NA && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, ldexpf(u, exps[t] + 133 - GV_TOP));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int t = 8 * (i / 4) + 2 * q + (i & 1), n = tl * 16 + g + 8 * ((i >> 1) & 1);
+                if (t < p.T && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, ldexpf(v[i], exps[t] + 133 - GV_TOP));
+            }
         }
-        if (whole && !last) put_tile<NT, F32, NA>(p, tile, g, q, acc);
+    };
+    bool whole = s == 0;  // the segment at hand starts at its tile's first step
+    auto finish = [&](bool ended) {
+        if constexpr (FEW) {  // add the four lanes that hold the row's groups; the other four hold none of it
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                float v = (q >> 1) == (g & 1) ? acc[i] : 0.0f;
+                v += __shfl_xor_sync(FULL, v, 1);
+                v += __shfl_xor_sync(FULL, v, 2);
+                acc[i] = v + __shfl_xor_sync(FULL, v, 4);
+            }
+        }
+        if (whole && ended) put_tile(tile, acc);
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < NA; ++i) red[(warp * NA + i) * 32 + lane] = acc[i];
         }
     };
-    auto use = [&](Step<NT> (&from)[GV_AHEAD], int z) {
+    int slot = 0;
+    for (int z = za; z < zb; ++z) {
+        cp_wait<GV_SLOTS - 2>();
+        __syncwarp();
+        const unsigned char *w = my_w + slot, *sc = my_s + slot;
+        if constexpr (FEW) {
+            few_step<TOK>(w, sc, x0[0] + s * xstep[0], xrow, my_g + 8 * s, 8 * steps, acc);
+        } else {
 #pragma unroll
-        for (int i = 0; i < GV_AHEAD; ++i) {
-            if (z + i >= zb) break;
-            const unsigned char* xp[NX];
+            for (int h = 0; h < 2; ++h) {
+                const unsigned char* xp[NX];
 #pragma unroll
-            for (int j = 0; j < NX; ++j) xp[j] = x0[j] + s * xstep[j];
-            if constexpr (NT == 0) few_step(from[i], xp[0], acc);
-            else row_step<NT>(from[i], xp, q, acc);
-            if (++s == steps) {
-                finish(false);
-                ++tile;
-                s = 0;
-                whole = true;
-#pragma unroll
-                for (int j = 0; j < NA; ++j) acc[j] = 0.0f;
+                for (int i = 0; i < NX; ++i) xp[i] = x0[i] + s * xstep[i] + h * (xstep[i] / 2);
+                row_step<NT>(w + 64 * h, sc + 8 * h, xp, my_g + (8 * s + 4 * h) * TOK, acc);
             }
         }
-    };
-    for (int z = za; z < zb; z += 2 * GV_AHEAD) {
-        fetch(st[1]);
-        use(st[0], z);
-        fetch(st[0]);
-        use(st[1], z + GV_AHEAD);
+        __syncwarp();  // the slot has been read
+        ask();
+        slot = slot + GV_SLOT == GV_RING ? 0 : slot + GV_SLOT;
+        if (++s == steps) {
+            finish(true);
+            ++tile;
+            s = 0;
+            whole = true;
+#pragma unroll
+            for (int i = 0; i < NA; ++i) acc[i] = 0.0f;
+        }
     }
     const bool open = zb > za && s != 0;  // the last segment ends inside its tile
-    if (open) finish(true);
+    if (open) finish(false);
     __syncthreads();
     if (!open || !whole) return;
     // this warp has the tile's first steps: the rest lies with the warps behind it
     const int end = (tile - ta + 1) * steps;
-    for (int w = warp + 1; w < WARPS && begin(w) < end; ++w) {
+    for (int w = warp + 1; w < warps && begin(w) < end; ++w) {
         if (begin(w) == begin(w + 1)) continue;
 #pragma unroll
         for (int i = 0; i < NA; ++i) acc[i] += red[(w * NA + i) * 32 + lane];
     }
-    put_tile<NT, F32, NA>(p, tile, g, q, acc);
+    put_tile(tile, acc);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -335,22 +419,17 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 
 using GemvKernel = void (*)(GemvParams);
 
-struct GemvPlan {
-    GemvKernel kern;
-    int warps, sums, blocks;  // warps a block, sums a lane, blocks an SM
-};
+template <bool F32>
+GemvKernel pick_gemv(int T, bool whole) {
+    if (T == 1) return whole ? gemv_kernel<-1, F32, true> : gemv_kernel<-1, F32, false>;
+    if (T == 2) return whole ? gemv_kernel<-2, F32, true> : gemv_kernel<-2, F32, false>;
+    if (T <= 8) return whole ? gemv_kernel<1, F32, true> : gemv_kernel<1, F32, false>;
+    if (T <= 16) return whole ? gemv_kernel<2, F32, true> : gemv_kernel<2, F32, false>;
+    return whole ? gemv_kernel<4, F32, true> : gemv_kernel<4, F32, false>;
+}
 
-template <bool F32, bool ALIGNED>
-GemvPlan plan_for(int T) {
-    if (T <= 2) return {gemv_kernel<0, F32, ALIGNED, 8>, 8, 2, 3};
-    if (T <= 8) return {gemv_kernel<1, F32, ALIGNED, 16>, 16, 4, 1};
-    if (T <= 16) return {gemv_kernel<2, F32, ALIGNED, 16>, 16, 8, 1};
-    return {gemv_kernel<4, F32, ALIGNED, 16>, 16, 16, 1};
-}
-GemvPlan plan_gemv(int T, bool f32, bool aligned) {
-    return f32 ? (aligned ? plan_for<true, true>(T) : plan_for<true, false>(T))
-               : (aligned ? plan_for<false, true>(T) : plan_for<false, false>(T));
-}
+int kept(int T) { return T <= 2 ? T : (T <= 8 ? 8 : (T <= 16 ? 16 : 32)); }    // tokens
+int sums(int T) { return T <= 2 ? 4 * T : (T <= 8 ? 4 : (T <= 16 ? 8 : 16)); }  // of a lane
 
 }  // namespace
 }  // namespace redmoe
@@ -380,27 +459,29 @@ extern "C" redmoe_status redmoe_gemv(const redmoe_matrix* W, const void* x, int3
     p.s = static_cast<const uint16_t*>(W->s);
     p.N = W->rows;
     p.K = W->cols;
-    // Token rows at a time: as many as fit in shared memory (all, at 32 rows of up to 2,944
-    // columns or 8 of up to 13,000), in whole blocks of eight where that is less than T. Each
-    // pass over W serves one such share.
-    const bool f32 = y_dtype == DT_F32, aligned128 = p.K % GV_STEP == 0;
-    const int steps = (p.K + GV_STEP - 1) / GV_STEP, tiles = (p.N + 15) / 16;
-    const int stride = steps * (2 * GV_STEP) + GV_PAD;
-    const int room = di.max_smem_optin - GV_ZERO - 16 * 16 * 32 * 4;
-    int most = room / stride;
-    if (most < T && most > 8) most -= most % 8;
-    if (most < 1) return REDMOE_ERR_UNSUPPORTED;
+    const bool f32 = y_dtype == DT_F32;
+    const int tiles = (p.N + 15) / 16, stride = row_stride(p.K);
+    // Token rows at a time: all, or as many as leave room for the shortest rings, in whole blocks of
+    // eight if more than that. Each pass over W serves one such share.
+    const int groups = (p.K + GV_COLS - 1) / GV_COLS * (GV_COLS / 32);
+    auto fixed_bytes = [&](int n) {
+        return n * stride + GV_ZERO + 128 + 4 * groups * kept(n) + GV_WARPS * sums(n) * 32 * 4;
+    };
+    int most = T;
+    while (most > 1 && fixed_bytes(most) + 8 * GV_RING > di.max_smem_optin)
+        most = most > 8 ? (most - 1) / 8 * 8 : most - 1;
     for (int t = 0; t < T; t += most) {
         p.T = T - t < most ? T - t : most;
         p.x = static_cast<const uint16_t*>(x) + size_t(t) * p.K;
         p.y = static_cast<char*>(y) + size_t(t) * p.N * (f32 ? 4 : 2);
-        const GemvPlan plan = plan_gemv(p.T, f32, aligned128);
-        const int smem = p.T * stride + GV_ZERO + plan.warps * plan.sums * 32 * 4;
+        const int fixed = fixed_bytes(p.T), room = (di.max_smem_optin - fixed) / GV_RING;
+        const int warps = room < GV_WARPS ? room : GV_WARPS;
+        const int smem = fixed + warps * GV_RING;
+        const GemvKernel kern = f32 ? pick_gemv<true>(p.T, p.K % GV_COLS == 0) : pick_gemv<false>(p.T, p.K % GV_COLS == 0);
         if (smem > 48 * 1024 &&
-            cudaFuncSetAttribute(plan.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return REDMOE_ERR_CUDA;
-        const int slots = plan.blocks * di.sm_count;
-        plan.kern<<<tiles < slots ? tiles : slots, 32 * plan.warps, smem, static_cast<cudaStream_t>(stream)>>>(p);
+        kern<<<tiles < di.sm_count ? tiles : di.sm_count, 32 * warps, smem, static_cast<cudaStream_t>(stream)>>>(p);
         if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
     }
     return REDMOE_OK;

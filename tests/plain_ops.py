@@ -147,10 +147,21 @@ def balance_backward(logits, counts, n, k, grad, mask=None):
 
 
 def gemv_rows(w, s, x, rows=None):
-    """x W^T and sum |x W| for the int4 group-32 matrix (rows: only those of W)."""
+    """x W^T, sum |x W| and sum |x| scale for the int4 group-32 matrix (rows: only those of W)."""
     w, s, x = w.cpu(), s.cpu(), d(x)
     if rows is not None:
         w, s = w[rows], s[rows]
     q = torch.stack(((w & 15).double(), (w >> 4).double()), dim=-1).reshape(w.shape[0], -1) - 8
-    W = q * s.double().repeat_interleave(32, dim=1)
-    return x @ W.T, x.abs() @ W.abs().T
+    S = s.double().repeat_interleave(32, dim=1)
+    return x @ (q * S).T, x.abs() @ (q * S).abs().T, x.abs() @ S.abs().T
+
+
+def gemv_err(m, ms, K):
+    """Bound on the kernel's error from sum |x W| and sum |x| scale, in exact arithmetic's place:
+
+    A group's sum starts at -8 X, X the fp32 sum of its 32 x: 8 additions of a lane and two of its
+    quad, 10 U sum |x|, so 80 U. Eight tensor-core accumulations follow over nibbles of 0 .. 15; each
+    may round or truncate (2 U) a partial sum of at most (8 + 15) sum |x|: 368 U. Then one U for the
+    product with the scale and one for each of the K / 32 additions and up to 16 + 3 more (warps,
+    lanes), of partial sums of |x W|."""
+    return U * (448 * ms + (K / 32 + 20) * (m + 448 * U * ms))

@@ -43,7 +43,6 @@
 namespace redmoe {
 namespace {
 
-constexpr int GV_WARPS = 16;
 constexpr int GV_MAX_T = 32;
 constexpr int GV_MAX_K = 65536;
 constexpr int GV_COLS = 256;     // columns of a step
@@ -51,9 +50,6 @@ constexpr int GV_PAD = 64;       // bytes between token rows of x in shared memo
 constexpr int GV_ZERO = 256;     // bytes of zeros: half a step of an absent token
 constexpr int GV_WROW = GV_COLS / 2 + 16;                  // bytes of a slot's row of W (bank offset)
 constexpr int GV_SROW = GV_COLS / 16;                      // bytes of a slot's row of scales
-constexpr int GV_SLOT = 16 * (GV_WROW + GV_SROW);
-constexpr int GV_SLOTS = 4;      // of a warp's ring: three steps in flight while one is used
-constexpr int GV_RING = GV_SLOTS * GV_SLOT;
 
 struct GemvParams {
     const uint8_t* w;      // [N, K/2]
@@ -86,82 +82,107 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
-// The exponent that a row's largest x is scaled to: the largest with room for rounding sums.
+// The exponent that a row's largest x is scaled to: the largest with room for its sums.
 constexpr int GV_TOP = 126;
 
-// x's T rows in shared memory as B wants them: every run of eight columns in the order (0,4)
-// (1,5)/16 (2,6) (3,7)/16, times 2^(GV_TOP - e) with e the exponent of the row's largest finite
-// element; zeros beyond K, and GV_ZERO of them behind. gsum: -8 times the sum of each group, in
-// the units of the products (FEW: [token][group], else [group][token]). exps[t] = e.
+// Ask for x's T rows in shared memory (zeros beyond K).
+__device__ __forceinline__ void fetch_x(const GemvParams& p, int stride, unsigned char* xs) {
+    const int runs = (stride - GV_PAD) / 16;  // of eight columns, 32 a step
+    for (int i = threadIdx.x; i < p.T * runs; i += blockDim.x) {
+        const int t = i / runs, r = i - t * runs;
+        unsigned char* dst = xs + t * stride + 16 * r;
+        if (8 * r < p.K) cp_async16(smem_u32(dst), p.x + size_t(t) * p.K + 8 * r);
+        else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pow2_pair(int e) { return uint32_t(127 + e) * 0x00800080u; }  // bf16 (2^e, 2^e)
+
+// Once this thread's part of fetch_x has arrived: x as B wants it. Every run of eight columns in
+// the order (0,4) (1,5)/16 (2,6) (3,7)/16, times 2^(GV_TOP - e) with e the exponent of the row's
+// largest element; exps[t] = e. gsum: -8 times the sum of each group in the units of the products
+// (FEW: [token][group], else [group][token]), made by the products themselves with a tile of
+// eights. tops: scratch, one word per 256 columns and token.
 template <bool FEW, int TOK>
-__device__ __forceinline__ void stage_x(const GemvParams& p, int stride, unsigned char* xs, float* gsum, int* exps) {
-    const int runs = (stride - GV_PAD) / 16;  // a multiple of 32: a warp's lanes are in one row
-    for (int i = threadIdx.x; i < TOK; i += blockDim.x) exps[i] = 0;
-    if (threadIdx.x < GV_ZERO / 16)
-        *reinterpret_cast<uint4*>(xs + size_t(p.T) * stride + 16 * threadIdx.x) = make_uint4(0u, 0u, 0u, 0u);
-    if (!FEW) {  // absent tokens
-        for (int i = threadIdx.x; i < runs / 4 * TOK; i += blockDim.x)
-            if (i % TOK >= p.T) gsum[i] = 0.0f;
+__device__ __forceinline__ void shape_x(const GemvParams& p, int stride, unsigned char* xs, const unsigned char* zero,
+                                        float* gsum, int* exps, uint32_t* tops) {
+    const int runs = (stride - GV_PAD) / 16, steps = runs / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int i = warp; i < p.T * steps; i += warps) {  // the runs this thread asked for
+        const int t = i / steps, r = (i - t * steps) * 32 + lane;
+        const uint4 v = *reinterpret_cast<const uint4*>(xs + t * stride + 16 * r);
+        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        const uint32_t top = __reduce_max_sync(FULL, max(m & 0xffffu, m >> 16));
+        if (lane == 0) tops[i] = top;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * runs; i += blockDim.x) {
-        const int t = i / runs, r = i - t * runs;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (8 * r < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + size_t(t) * p.K + 8 * r));
-        *reinterpret_cast<uint4*>(xs + size_t(t) * stride + 16 * r) = v;
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t top = 0;  // largest magnitude as a bit pattern; infinities and NaN do not count
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
-            if (lo < 0x7f80u) top = max(top, lo);
-            if (hi < 0x7f80u) top = max(top, hi);
-        }
+    for (int i = warp; i < p.T * steps; i += warps) {
+        const int t = i / steps, r = (i - t * steps) * 32 + lane;
+        uint32_t top = 0;
+        for (int k = lane; k < steps; k += 32) top = max(top, tops[t * steps + k]);
         top = __reduce_max_sync(FULL, top);
-        if ((threadIdx.x & 31) == 0) atomicMax(&exps[t], int(top));
+        // e is -126 (also for rows of subnormals) .. 128 (infinity or NaN); the scale as two factors
+        const int e = max(int(top >> 7), 1) - 127, up = GV_TOP - e, f0 = up / 2, f1 = up - f0;
+        const uint32_t a = pow2_pair(f0), b = pow2_pair(f1), c = pow2_pair(f1 - 4);
+        uint4* at = reinterpret_cast<uint4*>(xs + t * stride + 16 * r);
+        const uint4 v = *at;
+        *at = make_uint4(mul2(mul2(__byte_perm(v.x, v.z, 0x5410), a), b), mul2(mul2(__byte_perm(v.x, v.z, 0x7632), a), c),
+                         mul2(mul2(__byte_perm(v.y, v.w, 0x5410), a), b), mul2(mul2(__byte_perm(v.y, v.w, 0x7632), a), c));
+        if (lane == 0 && r == 0) exps[t] = e;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * runs; i += blockDim.x) {
-        const int t = i / runs, r = i - t * runs;
-        // the scale 2^(GV_TOP - e) as two factors: e is -126 .. 127 (rows of subnormals: -126)
-        const int e = max(exps[t] >> 7, 1) - 127, up = GV_TOP - e;
-        const float f0 = __int_as_float((127 + up / 2) << 23), f1 = __int_as_float((127 + up - up / 2) << 23);
-        const uint4 v = *reinterpret_cast<const uint4*>(xs + size_t(t) * stride + 16 * r);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float f[8], s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = bf16lo(w[j]) * f0 * f1;
-            f[2 * j + 1] = bf16hi(w[j]) * f0 * f1;
-            s += f[2 * j] * 0x1p-64f + f[2 * j + 1] * 0x1p-64f;
+    constexpr int NB = FEW ? 1 : TOK / 8;  // blocks of eight tokens
+    const int g = lane >> 2, q = lane & 3;
+    for (int i = warp; i < 8 * steps * NB; i += warps) {
+        const int group = i / NB, t0 = 8 * (i - group * NB);
+        const uint4 x = *reinterpret_cast<const uint4*>((t0 + g < p.T ? xs + (t0 + g) * stride + 64 * group : zero) + 16 * q);
+        float d[4];
+        mma_word(d, 0x88888888u, 0x88888888u, x, 0.0f, 0.0f, 0.0f, 0.0f);
+        if (g == 0) {  // every row of the sums is the same; this lane has tokens t0 + 2 q and the next
+            const int t = t0 + 2 * q;
+            if (FEW) {
+                if (t < TOK) gsum[t * 8 * steps + group] = -d[0];
+                if (t + 1 < TOK) gsum[(t + 1) * 8 * steps + group] = -d[1];
+            } else {
+                *reinterpret_cast<float2*>(gsum + group * TOK + t) = make_float2(-d[0], -d[1]);
+            }
         }
-        s += __shfl_xor_sync(FULL, s, 1);
-        s += __shfl_xor_sync(FULL, s, 2);
-        const float k = 0.0625f;
-        auto pair = [](float lo, float hi) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-            return *reinterpret_cast<const uint32_t*>(&h);
-        };
-        *reinterpret_cast<uint4*>(xs + size_t(t) * stride + 16 * r) =
-            make_uint4(pair(f[0], f[4]), pair(f[1] * k, f[5] * k), pair(f[2], f[6]), pair(f[3] * k, f[7] * k));
-        if ((r & 3) == 0) gsum[FEW ? t * (runs / 4) + r / 4 : (r / 4) * TOK + t] = s * -0x1p-66f;  // -8 2^(64 - 133)
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T; i += blockDim.x) exps[i] = max(exps[i] >> 7, 1) - 127;
     __syncthreads();
 }
 
+// What a pass over NT blocks of eight tokens, or (NT < 0) over -NT single ones, uses.
+template <int NT> struct Plan {
+    static constexpr bool FEW = NT <= 0;
+    static constexpr int TOK = FEW ? -NT : 8 * NT;  // tokens that sums are kept for
+    static constexpr int M = NT == 1 ? 2 : 1;       // tiles of 16 rows in a step: x is read once for them
+    static constexpr int WARPS = NT == -1 ? 24 : 16;               // at most
+    static constexpr int ROWS = 16 * M;
+    static constexpr int NA = M * 4 * (FEW ? TOK : NT);            // sums a lane holds
+    static constexpr int SLOTS = 3;                                // of a warp's ring
+    static constexpr int SLOT = ROWS * (GV_WROW + GV_SROW);
+    static constexpr int WARP_BYTES = SLOTS * SLOT + NA * 32 * 4;  // shared memory of a warp
+    static constexpr int fixed_bytes(int T, int K) {               // and of a block besides
+        return T * row_stride(K) + GV_ZERO + 128 + 16 + 4 * (8 * TOK + T) * ((K + GV_COLS - 1) / GV_COLS);
+    }
+};
+
 // Position in a warp's share of steps, with the lane's first address there: eight lanes read 128
 // bytes of a row, lane l chunk l % 8 of rows l / 8 + 4 j.
+template <int ROWS>
 struct Cursor {
     const uint8_t* w;
-    const uint16_t* sc;  // scales of row lane % 16
+    const uint16_t* sc;  // scales of row lane % ROWS
     int tile, s;
     __device__ __forceinline__ void at(const GemvParams& p, int tile_, int s_, int lane) {
         tile = tile_;
         s = s_;
-        w = p.w + size_t(tile * 16 + lane / 8) * (p.K / 2) + size_t(s) * (GV_COLS / 2) + 16 * (lane % 8);
-        sc = p.s + size_t(tile * 16 + lane % 16) * (p.K / 32) + s * (GV_COLS / 32);
+        w = p.w + size_t(tile * ROWS + lane / 8) * (p.K / 2) + size_t(s) * (GV_COLS / 2) + 16 * (lane % 8);
+        sc = p.s + size_t(tile * ROWS + lane % ROWS) * (p.K / 32) + s * (GV_COLS / 32);
     }
     __device__ __forceinline__ void next(const GemvParams& p, int steps, int lane) {
         w += GV_COLS / 2;
@@ -173,103 +194,108 @@ struct Cursor {
 // Ask for one step. Rows beyond N and columns beyond K keep what the slot holds: any code is
 // finite and meets a zero x or an output that is not stored. Scales beyond K are zeroed (what
 // lies there need not be finite). WHOLE: K % 256 == 0, a row's scales of a step are 16 bytes.
-template <bool WHOLE>
-__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor& c, int lane, unsigned char* slot) {
+template <bool WHOLE, int ROWS>
+__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<ROWS>& c, int lane, unsigned char* slot) {
     const uint32_t dst = smem_u32(slot) + (lane / 8) * GV_WROW + 16 * (lane % 8);
     const int groups = p.K / 32 - c.s * (GV_COLS / 32);  // groups left in the row
-    const size_t step4 = size_t(p.K) * 2;  // bytes of four rows
+    const size_t step4 = size_t(p.K) * 2;                // bytes of four rows
     if (WHOLE || lane % 8 < groups) {
-        if (c.tile * 16 + 16 <= p.N) {
+        if (c.tile * ROWS + ROWS <= p.N) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
+            for (int j = 0; j < ROWS / 4; ++j) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c.tile * 16 + lane / 8 + 4 * j < p.N) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
+            for (int j = 0; j < ROWS / 4; ++j)
+                if (c.tile * ROWS + lane / 8 + 4 * j < p.N) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
         }
     }
-    unsigned char* ss = slot + 16 * GV_WROW + (lane % 16) * GV_SROW;
-    if (c.tile * 16 + lane % 16 < p.N) {
+    unsigned char* ss = slot + ROWS * GV_WROW + (lane % ROWS) * GV_SROW;
+    if (c.tile * ROWS + lane % ROWS < p.N) {
         if (WHOLE) {
-            if (lane < 16) cp_async16(smem_u32(ss), c.sc);
+            if (lane < ROWS) cp_async16(smem_u32(ss), c.sc);
         } else {
+            constexpr int EACH = 8 * ROWS / 32;  // scales a lane fetches
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = 4 * (lane / 16) + i;
+            for (int i = 0; i < EACH; ++i) {
+                const int k = EACH * (lane / ROWS) + i;
                 reinterpret_cast<uint16_t*>(ss)[k] = k < groups ? __ldg(c.sc + k) : uint16_t(0);
             }
         }
     }
 }
 
-// One or two tokens, 16 rows by 256 columns: lane (g, q) reads chunk q + 4 (g & 1) of rows
+// One or two tokens, M tiles of 16 rows by 256 columns: lane (g, q) reads chunk q + 4 (g & 1) of rows
 // g / 2 + 4 j. The rows g of an mma are a W row's first four groups (g even) and its last four
 // (g odd): columns 2 q, 2 q + 1 of a lane's sums count where they are that half's.
-// w: the lane's first chunk, s: the first row's scales, x: the lane's column of B (zeros in the
-// lanes that hold other groups), xrow bytes from one token's to the next.
-// gs: this lane's pair of group sums, grow floats from one token's to the next.
-template <int TOK>
-__device__ __forceinline__ void few_step(const unsigned char* w, const unsigned char* s, const unsigned char* x, int xrow,
-                                         const float* gs, int grow, float (&acc)[4 * TOK]) {
-    float cc[TOK][2][4];
-    uint4 v[4];
-    uint32_t sc[4];
+// w: the lane's first chunk, s: the first row's scales; `release` is called once they are read.
+// x: the lane's column of B (zeros in the lanes that hold other groups), xrow bytes from one
+// token's to the next. gs: this lane's pair of group sums, grow floats apart.
+template <int TOK, int M, class Release>
+__device__ __forceinline__ void few_step(const unsigned char* w, const unsigned char* s, Release release,
+                                         const unsigned char* x, int xrow, const float* gs, int grow,
+                                         float (&acc)[4 * M * TOK]) {
+    uint4 v[4 * M];
+    uint32_t sc[4 * M];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * GV_WROW);
-        sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * GV_SROW);
-    }
+    for (int j = 0; j < 4 * M; ++j) v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * GV_WROW);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4 * M; ++j) sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * GV_SROW);
+    release();
 #pragma unroll
-        for (int t = 0; t < TOK; ++t) {
+    for (int t = 0; t < TOK; ++t) {
+        float cc[2 * M][4];
+        const float2 c = *reinterpret_cast<const float2*>(gs + t * grow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             const uint4 xv = *reinterpret_cast<const uint4*>(x + t * xrow + 16 * i);
-            const float2 c = i == 0 ? *reinterpret_cast<const float2*>(gs + t * grow) : make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2 * M; ++h) {
                 const uint4 va = v[2 * h], vb = v[2 * h + 1];
                 const uint32_t a = i == 0 ? va.x : i == 1 ? va.y : i == 2 ? va.z : va.w;
                 const uint32_t b = i == 0 ? vb.x : i == 1 ? vb.y : i == 2 ? vb.z : vb.w;
-                float(&d)[4] = cc[t][h];
+                float(&d)[4] = cc[h];
                 if (i == 0) mma_word(d, a, b, xv, c.x, c.y, c.x, c.y);
                 else mma_word(d, a, b, xv, d[0], d[1], d[2], d[3]);
             }
         }
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float s0 = bf16lo(sc[j]), s1 = bf16hi(sc[j]);
-#pragma unroll
-        for (int t = 0; t < TOK; ++t) {
-            const int k = 4 * t + j, c = 2 * (j & 1);
-            acc[k] = fmaf(cc[t][j / 2][c], s0, fmaf(cc[t][j / 2][c + 1], s1, acc[k]));
+        for (int j = 0; j < 4 * M; ++j) {
+            const int k = 4 * M * t + j, e = 2 * (j & 1);
+            acc[k] = fmaf(cc[j / 2][e], bf16lo(sc[j]), fmaf(cc[j / 2][e + 1], bf16hi(sc[j]), acc[k]));
         }
     }
 }
 
-// Eight NT tokens, 16 rows by 128 columns: lane (g, q) reads its quarter of the four groups of
-// rows g and g + 8; x holds the lane's token of each block of eight, gs the group sums of the
-// lane's two tokens of C in the first block.
-template <int NT>
+// Eight NT tokens, M tiles of 16 rows by 128 columns: lane (g, q) reads its quarter of the four
+// groups of rows g and g + 8; x holds the lane's token of each block of eight, gs the group sums
+// of the lane's two tokens of C in the first block.
+template <int NT, int M>
 __device__ __forceinline__ void row_step(const unsigned char* w, const unsigned char* s, const unsigned char* const (&x)[NT],
-                                         const float* gs, float (&acc)[4 * NT]) {
-    const uint2 sa = *reinterpret_cast<const uint2*>(s), sb = *reinterpret_cast<const uint2*>(s + 8 * GV_SROW);
+                                         const float* gs, float (&acc)[4 * NT * M]) {
+    uint2 sc[2 * M];
+#pragma unroll
+    for (int m = 0; m < 2 * M; ++m) sc[m] = *reinterpret_cast<const uint2*>(s + 8 * m * GV_SROW);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t a = *reinterpret_cast<const uint32_t*>(w + 16 * i);
-        const uint32_t b = *reinterpret_cast<const uint32_t*>(w + 8 * GV_WROW + 16 * i);
-        const uint32_t ua = i < 2 ? sa.x : sa.y, ub = i < 2 ? sb.x : sb.y;
-        const float fa = i & 1 ? bf16hi(ua) : bf16lo(ua), fb = i & 1 ? bf16hi(ub) : bf16lo(ub);
+        uint32_t v[2 * M];
+#pragma unroll
+        for (int m = 0; m < 2 * M; ++m) v[m] = *reinterpret_cast<const uint32_t*>(w + 8 * m * GV_WROW + 16 * i);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint4 v = *reinterpret_cast<const uint4*>(x[nt] + 64 * i);
+            const uint4 xv = *reinterpret_cast<const uint4*>(x[nt] + 64 * i);
             const float2 c = *reinterpret_cast<const float2*>(gs + i * (8 * NT) + 8 * nt);
-            float cc[4];
-            mma_word(cc, a, b, v, c.x, c.y, c.x, c.y);
-            acc[4 * nt + 0] = fmaf(cc[0], fa, acc[4 * nt + 0]);
-            acc[4 * nt + 1] = fmaf(cc[1], fa, acc[4 * nt + 1]);
-            acc[4 * nt + 2] = fmaf(cc[2], fb, acc[4 * nt + 2]);
-            acc[4 * nt + 3] = fmaf(cc[3], fb, acc[4 * nt + 3]);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const uint32_t ua = i < 2 ? sc[2 * m].x : sc[2 * m].y, ub = i < 2 ? sc[2 * m + 1].x : sc[2 * m + 1].y;
+                const float fa = i & 1 ? bf16hi(ua) : bf16lo(ua), fb = i & 1 ? bf16hi(ub) : bf16lo(ub);
+                float cc[4];
+                mma_word(cc, v[2 * m], v[2 * m + 1], xv, c.x, c.y, c.x, c.y);
+                float* to = acc + 4 * (m * NT + nt);
+                to[0] = fmaf(cc[0], fa, to[0]);
+                to[1] = fmaf(cc[1], fa, to[1]);
+                to[2] = fmaf(cc[2], fb, to[2]);
+                to[3] = fmaf(cc[3], fb, to[3]);
+            }
         }
     }
 }
@@ -282,11 +308,11 @@ __device__ __forceinline__ void put(void* y, size_t i, float v) {
 
 // NT < 0: -NT tokens (one or two); otherwise NT blocks of eight. All of x in shared memory.
 template <int NT, bool F32, bool WHOLE>
-__global__ void __launch_bounds__(32 * GV_WARPS, 1) gemv_kernel(const GemvParams p) {
+__global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const GemvParams p) {
     extern __shared__ __align__(16) unsigned char sm[];
-    constexpr bool FEW = NT <= 0;
-    constexpr int TOK = FEW ? -NT : 8 * NT;
-    constexpr int NA = FEW ? 4 * TOK : 4 * NT;  // sums a lane holds
+    using P = Plan<NT>;
+    constexpr bool FEW = P::FEW;
+    constexpr int TOK = P::TOK, NA = P::NA, ROWS = P::ROWS, RING = P::SLOTS * P::SLOT;
     const int steps = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int g = lane >> 2, q = lane & 3;
@@ -294,31 +320,36 @@ __global__ void __launch_bounds__(32 * GV_WARPS, 1) gemv_kernel(const GemvParams
     unsigned char* zero = xs + size_t(p.T) * stride;
     int* exps = reinterpret_cast<int*>(zero + GV_ZERO);     // [TOK], in 128 bytes
     float* gsum = reinterpret_cast<float*>(exps + 32);      // [TOK][8 steps] or [8 steps][TOK]
-    float* red = gsum + TOK * 8 * steps;                    // [warps][NA][32]
-    unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * GV_RING;
+    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + TOK * 8 * steps);        // [T][steps]
+    float* red = reinterpret_cast<float*>(tops + (p.T * steps + 3) / 4 * 4);     // [warps][NA][32]
+    unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * RING;
 
-    const int ntiles = (p.N + 15) / 16;
+    const int ntiles = (p.N + ROWS - 1) / ROWS;
     const int ta = int((long long)ntiles * blockIdx.x / gridDim.x), tb = int((long long)ntiles * (blockIdx.x + 1) / gridDim.x);
     // at most 2^24 tiles over 148 blocks or more, of 256 steps: total * warps < 2^30
     const int total = (tb - ta) * steps;
     auto begin = [&](int w) { return total * w / warps; };
     const int za = begin(warp), zb = begin(warp + 1);
 
-    Cursor in;
+    Cursor<ROWS> in;
     in.at(p, ta + za / steps, za % steps, lane);
     int tile = in.tile, s = in.s, zin = za, sin = 0;
     auto ask = [&]() {  // one group per call, an empty one behind the last step
         if (zin < zb) {
-            fetch<WHOLE>(p, in, lane, ring + sin);
+            fetch<WHOLE, ROWS>(p, in, lane, ring + sin);
             in.next(p, steps, lane);
-            sin = sin + GV_SLOT == GV_RING ? 0 : sin + GV_SLOT;
+            sin = sin + P::SLOT == RING ? 0 : sin + P::SLOT;
             ++zin;
         }
         cp_commit();
     };
-    #pragma unroll
-    for (int i = 0; i < GV_SLOTS - 1; ++i) ask();
-    stage_x<FEW, TOK>(p, stride, xs, gsum, exps);
+        fetch_x(p, stride, xs);
+    cp_commit();
+#pragma unroll
+    for (int i = 0; i < P::SLOTS - 1; ++i) ask();
+    if (threadIdx.x < GV_ZERO / 16) reinterpret_cast<uint4*>(zero)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    cp_wait<P::SLOTS - 1>();
+    shape_x<FEW, TOK>(p, stride, xs, zero, gsum, exps, tops);
 
     const int xrow = FEW && (g & 3) == q ? stride : 0;
     constexpr int NX = FEW ? 1 : NT;
@@ -331,22 +362,24 @@ __global__ void __launch_bounds__(32 * GV_WARPS, 1) gemv_kernel(const GemvParams
         xstep[i] = there ? 2 * GV_COLS : 0;
     }
     const unsigned char* my_w = ring + (FEW ? (lane / 8) * GV_WROW + 16 * (lane % 8) : g * GV_WROW + 4 * q);
-    const unsigned char* my_s = ring + 16 * GV_WROW + (FEW ? (lane / 8) * GV_SROW + 4 * q : g * GV_SROW);
+    const unsigned char* my_s = ring + ROWS * GV_WROW + (FEW ? (lane / 8) * GV_SROW + 4 * q : g * GV_SROW);
     const float* my_g = gsum + 2 * q;
 
     float acc[NA] = {};
     auto put_tile = [&](int tl, const float (&v)[NA]) {
-        if constexpr (FEW) {
-            const int m = lane % 8;  // the sums are in all eight lanes of a row: lane m stores sum m
-            float u = v[0];
+        if constexpr (FEW) {  // the sums are in all eight lanes of a row: lane m stores sum m of each token
+            const int m = lane % 8, n = tl * ROWS + lane / 8 + 4 * m;
 #pragma unroll
-            for (int i = 1; i < NA; ++i) u = m == i ? v[i] : u;
-            const int n = tl * 16 + lane / 8 + 4 * (m & 3), t = m >> 2;
-            if (m < NA && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, ldexpf(u, exps[t] + 133 - GV_TOP));
+            for (int t = 0; t < TOK; ++t) {
+                float u = v[4 * P::M * t];
+#pragma unroll
+                for (int i = 1; i < 4 * P::M; ++i) u = m == i ? v[4 * P::M * t + i] : u;
+                if (m < 4 * P::M && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, ldexpf(u, exps[t] + 133 - GV_TOP));
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
-                const int t = 8 * (i / 4) + 2 * q + (i & 1), n = tl * 16 + g + 8 * ((i >> 1) & 1);
+                const int t = 8 * (i / 4 % NT) + 2 * q + (i & 1), n = tl * ROWS + 16 * (i / (4 * NT)) + g + 8 * ((i >> 1) & 1);
                 if (t < p.T && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, ldexpf(v[i], exps[t] + 133 - GV_TOP));
             }
         }
@@ -370,23 +403,26 @@ __global__ void __launch_bounds__(32 * GV_WARPS, 1) gemv_kernel(const GemvParams
     };
     int slot = 0;
     for (int z = za; z < zb; ++z) {
-        cp_wait<GV_SLOTS - 2>();
+        cp_wait<P::SLOTS - 2>();
         __syncwarp();
         const unsigned char *w = my_w + slot, *sc = my_s + slot;
+        auto release = [&]() {
+            __syncwarp();  // the slot has been read
+            ask();
+        };
         if constexpr (FEW) {
-            few_step<TOK>(w, sc, x0[0] + s * xstep[0], xrow, my_g + 8 * s, 8 * steps, acc);
+            few_step<TOK, P::M>(w, sc, release, x0[0] + s * xstep[0], xrow, my_g + 8 * s, 8 * steps, acc);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const unsigned char* xp[NX];
 #pragma unroll
                 for (int i = 0; i < NX; ++i) xp[i] = x0[i] + s * xstep[i] + h * (xstep[i] / 2);
-                row_step<NT>(w + 64 * h, sc + 8 * h, xp, my_g + (8 * s + 4 * h) * TOK, acc);
+                row_step<NT, P::M>(w + 64 * h, sc + 8 * h, xp, my_g + (8 * s + 4 * h) * TOK, acc);
             }
+            release();
         }
-        __syncwarp();  // the slot has been read
-        ask();
-        slot = slot + GV_SLOT == GV_RING ? 0 : slot + GV_SLOT;
+        slot = slot + P::SLOT == RING ? 0 : slot + P::SLOT;
         if (++s == steps) {
             finish(true);
             ++tile;
@@ -417,19 +453,38 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     return a && b && x < y + bn && y < x + an;
 }
 
-using GemvKernel = void (*)(GemvParams);
-
-template <bool F32>
-GemvKernel pick_gemv(int T, bool whole) {
-    if (T == 1) return whole ? gemv_kernel<-1, F32, true> : gemv_kernel<-1, F32, false>;
-    if (T == 2) return whole ? gemv_kernel<-2, F32, true> : gemv_kernel<-2, F32, false>;
-    if (T <= 8) return whole ? gemv_kernel<1, F32, true> : gemv_kernel<1, F32, false>;
-    if (T <= 16) return whole ? gemv_kernel<2, F32, true> : gemv_kernel<2, F32, false>;
-    return whole ? gemv_kernel<4, F32, true> : gemv_kernel<4, F32, false>;
+// One pass over W for p.T tokens.
+template <int NT, bool F32, bool WHOLE>
+bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
+    using P = Plan<NT>;
+    const int fixed = P::fixed_bytes(p.T, p.K), room = (di.max_smem_optin - fixed) / P::WARP_BYTES;
+    const int warps = room < P::WARPS ? room : P::WARPS, smem = fixed + warps * P::WARP_BYTES;
+    const auto kern = gemv_kernel<NT, F32, WHOLE>;
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return false;
+    const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
+    kern<<<tiles < di.sm_count ? tiles : di.sm_count, 32 * warps, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess;
 }
 
-int kept(int T) { return T <= 2 ? T : (T <= 8 ? 8 : (T <= 16 ? 16 : 32)); }    // tokens
-int sums(int T) { return T <= 2 ? 4 * T : (T <= 8 ? 4 : (T <= 16 ? 8 : 16)); }  // of a lane
+// Whether T tokens of K columns leave room for eight warps' rings.
+bool fits(int T, int K, int smem) {
+    const int need = T == 1   ? Plan<-1>::fixed_bytes(T, K) + 8 * Plan<-1>::WARP_BYTES
+                     : T == 2 ? Plan<-2>::fixed_bytes(T, K) + 8 * Plan<-2>::WARP_BYTES
+                     : T <= 8 ? Plan<1>::fixed_bytes(T, K) + 8 * Plan<1>::WARP_BYTES
+                     : T <= 16 ? Plan<2>::fixed_bytes(T, K) + 8 * Plan<2>::WARP_BYTES
+                               : Plan<4>::fixed_bytes(T, K) + 8 * Plan<4>::WARP_BYTES;
+    return need <= smem;
+}
+
+template <bool F32, bool WHOLE>
+bool launch_tokens(const GemvParams& p, const DevInfo& di, cudaStream_t s) {
+    if (p.T == 1) return launch_gemv<-1, F32, WHOLE>(p, di, s);
+    if (p.T == 2) return launch_gemv<-2, F32, WHOLE>(p, di, s);
+    if (p.T <= 8) return launch_gemv<1, F32, WHOLE>(p, di, s);
+    if (p.T <= 16) return launch_gemv<2, F32, WHOLE>(p, di, s);
+    return launch_gemv<4, F32, WHOLE>(p, di, s);
+}
 
 }  // namespace
 }  // namespace redmoe
@@ -459,30 +514,19 @@ extern "C" redmoe_status redmoe_gemv(const redmoe_matrix* W, const void* x, int3
     p.s = static_cast<const uint16_t*>(W->s);
     p.N = W->rows;
     p.K = W->cols;
-    const bool f32 = y_dtype == DT_F32;
-    const int tiles = (p.N + 15) / 16, stride = row_stride(p.K);
-    // Token rows at a time: all, or as many as leave room for the shortest rings, in whole blocks of
-    // eight if more than that. Each pass over W serves one such share.
-    const int groups = (p.K + GV_COLS - 1) / GV_COLS * (GV_COLS / 32);
-    auto fixed_bytes = [&](int n) {
-        return n * stride + GV_ZERO + 128 + 4 * groups * kept(n) + GV_WARPS * sums(n) * 32 * 4;
-    };
+    // Token rows at a time: all, or as many as leave room for eight rings, in whole blocks of eight
+    // if more than that. Each pass over W serves one such share.
     int most = T;
-    while (most > 1 && fixed_bytes(most) + 8 * GV_RING > di.max_smem_optin)
-        most = most > 8 ? (most - 1) / 8 * 8 : most - 1;
+    while (most > 1 && !fits(most, p.K, di.max_smem_optin)) most = most > 8 ? (most - 1) / 8 * 8 : most - 1;
+    const bool f32 = y_dtype == DT_F32, whole = p.K % GV_COLS == 0;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int t = 0; t < T; t += most) {
         p.T = T - t < most ? T - t : most;
         p.x = static_cast<const uint16_t*>(x) + size_t(t) * p.K;
         p.y = static_cast<char*>(y) + size_t(t) * p.N * (f32 ? 4 : 2);
-        const int fixed = fixed_bytes(p.T), room = (di.max_smem_optin - fixed) / GV_RING;
-        const int warps = room < GV_WARPS ? room : GV_WARPS;
-        const int smem = fixed + warps * GV_RING;
-        const GemvKernel kern = f32 ? pick_gemv<true>(p.T, p.K % GV_COLS == 0) : pick_gemv<false>(p.T, p.K % GV_COLS == 0);
-        if (smem > 48 * 1024 &&
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return REDMOE_ERR_CUDA;
-        kern<<<tiles < di.sm_count ? tiles : di.sm_count, 32 * warps, smem, static_cast<cudaStream_t>(stream)>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
+        const bool ok = f32 ? (whole ? launch_tokens<true, true>(p, di, st) : launch_tokens<true, false>(p, di, st))
+                            : (whole ? launch_tokens<false, true>(p, di, st) : launch_tokens<false, false>(p, di, st));
+        if (!ok) return REDMOE_ERR_CUDA;
     }
     return REDMOE_OK;
 }

@@ -85,14 +85,31 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 // The exponent that a row's largest x is scaled to: the largest with room for its sums.
 constexpr int GV_TOP = 126;
 
+// How the block's warps share x's rows while it is prepared: `parts` warps a row (one, and several
+// rows a warp, where there are more rows than warps), warp `part` of them on runs of eight columns
+// 32 part + lane, + 32 parts, ...
+struct RowShare {
+    int parts, part, first, step;
+    __device__ __forceinline__ explicit RowShare(int T) {
+        const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        parts = max(warps / T, 1);
+        part = warps >= T ? warp / T : 0;
+        first = warps >= T ? warp % T : warp;
+        if (part >= parts) first = T;  // a warp too many
+        step = warps >= T ? T : warps;
+    }
+};
+
 // Ask for x's T rows in shared memory (zeros beyond K).
-__device__ __forceinline__ void fetch_x(const GemvParams& p, int stride, unsigned char* xs) {
-    const int runs = (stride - GV_PAD) / 16;  // of eight columns, 32 a step
-    for (int i = threadIdx.x; i < p.T * runs; i += blockDim.x) {
-        const int t = i / runs, r = i - t * runs;
-        unsigned char* dst = xs + t * stride + 16 * r;
-        if (8 * r < p.K) cp_async16(smem_u32(dst), p.x + size_t(t) * p.K + 8 * r);
-        else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void fetch_x(const GemvParams& p, const RowShare& sh, int stride, unsigned char* xs) {
+    const int runs = (stride - GV_PAD) / 16, lane = threadIdx.x & 31;
+    for (int t = sh.first; t < p.T; t += sh.step) {
+#pragma unroll 4
+        for (int r = 32 * sh.part + lane; r < runs; r += 32 * sh.parts) {
+            unsigned char* dst = xs + t * stride + 16 * r;
+            if (8 * r < p.K) cp_async16(smem_u32(dst), p.x + size_t(t) * p.K + 8 * r);
+            else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
 }
 
@@ -106,37 +123,42 @@ __device__ __forceinline__ uint32_t pow2_pair(int e) { return uint32_t(127 + e) 
 // the order (0,4) (1,5)/16 (2,6) (3,7)/16, times 2^(GV_TOP - e) with e the exponent of the row's
 // largest element; exps[t] = e. gsum: -8 times the sum of each group in the units of the products
 // (FEW: [token][group], else [group][token]), made by the products themselves with a tile of
-// eights. tops: scratch, one word per 256 columns and token.
+// eights. tops: scratch, one word for each warp of each row.
 template <bool FEW, int TOK>
-__device__ __forceinline__ void shape_x(const GemvParams& p, int stride, unsigned char* xs, const unsigned char* zero,
+__device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh, int stride, unsigned char* xs, const unsigned char* zero,
                                         float* gsum, int* exps, uint32_t* tops) {
     const int runs = (stride - GV_PAD) / 16, steps = runs / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    for (int i = warp; i < p.T * steps; i += warps) {  // the runs this thread asked for
-        const int t = i / steps, r = (i - t * steps) * 32 + lane;
-        const uint4 v = *reinterpret_cast<const uint4*>(xs + t * stride + 16 * r);
-        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    for (int t = sh.first; t < p.T; t += sh.step) {  // the runs this thread asked for
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int r = 32 * sh.part + lane; r < runs; r += 32 * sh.parts) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xs + t * stride + 16 * r);
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
         const uint32_t top = __reduce_max_sync(FULL, max(m & 0xffffu, m >> 16));
-        if (lane == 0) tops[i] = top;
+        if (lane == 0) tops[sh.part * p.T + t] = top;
     }
     __syncthreads();
-    for (int i = warp; i < p.T * steps; i += warps) {
-        const int t = i / steps, r = (i - t * steps) * 32 + lane;
-        uint32_t top = 0;
-        for (int k = lane; k < steps; k += 32) top = max(top, tops[t * steps + k]);
-        top = __reduce_max_sync(FULL, top);
+    for (int t = sh.first; t < p.T; t += sh.step) {
+        const uint32_t top = __reduce_max_sync(FULL, lane < sh.parts ? tops[lane * p.T + t] : 0u);
         // e is -126 (also for rows of subnormals) .. 128 (infinity or NaN); the scale as two factors
         const int e = max(int(top >> 7), 1) - 127, up = GV_TOP - e, f0 = up / 2, f1 = up - f0;
         const uint32_t a = pow2_pair(f0), b = pow2_pair(f1), c = pow2_pair(f1 - 4);
-        uint4* at = reinterpret_cast<uint4*>(xs + t * stride + 16 * r);
-        const uint4 v = *at;
-        *at = make_uint4(mul2(mul2(__byte_perm(v.x, v.z, 0x5410), a), b), mul2(mul2(__byte_perm(v.x, v.z, 0x7632), a), c),
-                         mul2(mul2(__byte_perm(v.y, v.w, 0x5410), a), b), mul2(mul2(__byte_perm(v.y, v.w, 0x7632), a), c));
-        if (lane == 0 && r == 0) exps[t] = e;
+#pragma unroll 4
+        for (int r = 32 * sh.part + lane; r < runs; r += 32 * sh.parts) {
+            uint4* at = reinterpret_cast<uint4*>(xs + t * stride + 16 * r);
+            const uint4 v = *at;
+            *at = make_uint4(mul2(mul2(__byte_perm(v.x, v.z, 0x5410), a), b), mul2(mul2(__byte_perm(v.x, v.z, 0x7632), a), c),
+                             mul2(mul2(__byte_perm(v.y, v.w, 0x5410), a), b), mul2(mul2(__byte_perm(v.y, v.w, 0x7632), a), c));
+        }
+        if (lane == 0 && sh.part == 0) exps[t] = e;
     }
     __syncthreads();
     constexpr int NB = FEW ? 1 : TOK / 8;  // blocks of eight tokens
     const int g = lane >> 2, q = lane & 3;
+#pragma unroll 4
     for (int i = warp; i < 8 * steps * NB; i += warps) {
         const int group = i / NB, t0 = 8 * (i - group * NB);
         const uint4 x = *reinterpret_cast<const uint4*>((t0 + g < p.T ? xs + (t0 + g) * stride + 64 * group : zero) + 16 * q);
@@ -167,7 +189,7 @@ template <int NT> struct Plan {
     static constexpr int SLOT = ROWS * (GV_WROW + GV_SROW);
     static constexpr int WARP_BYTES = SLOTS * SLOT + NA * 32 * 4;  // shared memory of a warp
     static constexpr int fixed_bytes(int T, int K) {               // and of a block besides
-        return T * row_stride(K) + GV_ZERO + 128 + 16 + 4 * (8 * TOK + T) * ((K + GV_COLS - 1) / GV_COLS);
+        return T * row_stride(K) + GV_ZERO + 128 + 128 + 4 * 8 * TOK * ((K + GV_COLS - 1) / GV_COLS);
     }
 };
 
@@ -291,10 +313,9 @@ __device__ __forceinline__ void row_step(const unsigned char* w, const unsigned 
                 float cc[4];
                 mma_word(cc, v[2 * m], v[2 * m + 1], xv, c.x, c.y, c.x, c.y);
                 float* to = acc + 4 * (m * NT + nt);
-                to[0] = fmaf(cc[0], fa, to[0]);
-                to[1] = fmaf(cc[1], fa, to[1]);
-                to[2] = fmaf(cc[2], fb, to[2]);
-                to[3] = fmaf(cc[3], fb, to[3]);
+                const float2 u = __ffma2_rn(make_float2(cc[0], cc[1]), make_float2(fa, fa), make_float2(to[0], to[1]));
+                const float2 v2 = __ffma2_rn(make_float2(cc[2], cc[3]), make_float2(fb, fb), make_float2(to[2], to[3]));
+                to[0] = u.x; to[1] = u.y; to[2] = v2.x; to[3] = v2.y;
             }
         }
     }
@@ -320,15 +341,15 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     unsigned char* zero = xs + size_t(p.T) * stride;
     int* exps = reinterpret_cast<int*>(zero + GV_ZERO);     // [TOK], in 128 bytes
     float* gsum = reinterpret_cast<float*>(exps + 32);      // [TOK][8 steps] or [8 steps][TOK]
-    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + TOK * 8 * steps);        // [T][steps]
-    float* red = reinterpret_cast<float*>(tops + (p.T * steps + 3) / 4 * 4);     // [warps][NA][32]
+    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + TOK * 8 * steps);  // 128 bytes
+    float* red = reinterpret_cast<float*>(tops + 32);                      // [warps][NA][32]
     unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * RING;
 
     const int ntiles = (p.N + ROWS - 1) / ROWS;
     const int ta = int((long long)ntiles * blockIdx.x / gridDim.x), tb = int((long long)ntiles * (blockIdx.x + 1) / gridDim.x);
-    // at most 2^24 tiles over 148 blocks or more, of 256 steps: total * warps < 2^30
-    const int total = (tb - ta) * steps;
-    auto begin = [&](int w) { return total * w / warps; };
+    // at most 2^24 tiles over 148 blocks or more, of 256 steps: total < 2^25
+    const int total = (tb - ta) * steps, each = total / warps, more = total - each * warps;
+    auto begin = [&](int w) { return w * each + min(w, more); };
     const int za = begin(warp), zb = begin(warp + 1);
 
     Cursor<ROWS> in;
@@ -343,13 +364,14 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
         }
         cp_commit();
     };
-        fetch_x(p, stride, xs);
+        const RowShare share(p.T);
+    fetch_x(p, share, stride, xs);
     cp_commit();
 #pragma unroll
     for (int i = 0; i < P::SLOTS - 1; ++i) ask();
     if (threadIdx.x < GV_ZERO / 16) reinterpret_cast<uint4*>(zero)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     cp_wait<P::SLOTS - 1>();
-    shape_x<FEW, TOK>(p, stride, xs, zero, gsum, exps, tops);
+    shape_x<FEW, TOK>(p, share, stride, xs, zero, gsum, exps, tops);
 
     const int xrow = FEW && (g & 3) == q ? stride : 0;
     constexpr int NX = FEW ? 1 : NT;

@@ -24,9 +24,9 @@
 //
 // An mma sums over the quad of lanes that shares its rows, so the quad must not mix groups:
 //
-//   one or two rows of x: the eight columns of B are eight groups. A lane holds one whole group
-//      (16 bytes) of one row; column j of B is x in the lane slots of group j and zero in the
-//      others, so one chain of eight products makes eight groups' sums of eight W rows.
+//   one row of x: the eight columns of B are eight groups. A lane holds one whole group (16 bytes)
+//      of one row; column j of B is x in the lane slots of group j and zero in the others, so one
+//      chain of eight products makes eight groups' sums of eight W rows.
 //   more rows: the eight columns of B are eight tokens, and a lane holds its quarter (4 bytes) of
 //      one group after the other.
 //
@@ -122,9 +122,9 @@ __device__ __forceinline__ uint32_t pow2_pair(int e) { return uint32_t(127 + e) 
 // Once this thread's part of fetch_x has arrived: x as B wants it. Every run of eight columns in
 // the order (0,4) (1,5)/16 (2,6) (3,7)/16, times 2^(GV_TOP - e) with e the exponent of the row's
 // largest element; exps[t] = e. gsum: -8 times the sum of each group in the units of the products
-// (FEW: [token][group], else [group][token]), made by the products themselves with a tile of
+// (ONE: [group], else [group][token pair] as the four numbers of C), made by the products themselves with a tile of
 // eights. tops: scratch, one word for each warp of each row.
-template <bool FEW, int TOK>
+template <bool ONE, int TOK>
 __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh, int stride, unsigned char* xs, const unsigned char* zero,
                                         float* gsum, int* exps, uint32_t* tops) {
     const int runs = (stride - GV_PAD) / 16, steps = runs / 32;
@@ -156,7 +156,7 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
         if (lane == 0 && sh.part == 0) exps[t] = e;
     }
     __syncthreads();
-    constexpr int NB = FEW ? 1 : TOK / 8;  // blocks of eight tokens
+    constexpr int NB = ONE ? 1 : TOK / 8;  // blocks of eight tokens
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll 4
     for (int i = warp; i < 8 * steps * NB; i += warps) {
@@ -166,30 +166,29 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
         mma_word(d, 0x88888888u, 0x88888888u, x, 0.0f, 0.0f, 0.0f, 0.0f);
         if (g == 0) {  // every row of the sums is the same; this lane has tokens t0 + 2 q and the next
             const int t = t0 + 2 * q;
-            if (FEW) {
-                if (t < TOK) gsum[t * 8 * steps + group] = -d[0];
-                if (t + 1 < TOK) gsum[(t + 1) * 8 * steps + group] = -d[1];
+            if (ONE) {
+                if (t == 0) gsum[group] = -d[0];
             } else {
-                *reinterpret_cast<float2*>(gsum + group * TOK + t) = make_float2(-d[0], -d[1]);
+                *reinterpret_cast<float4*>(gsum + 2 * (group * TOK + t)) = make_float4(-d[0], -d[1], -d[0], -d[1]);
             }
         }
     }
     __syncthreads();
 }
 
-// What a pass over NT blocks of eight tokens, or (NT < 0) over -NT single ones, uses.
+// What a pass over NT blocks of eight tokens, or (NT = 0) over one token, uses.
 template <int NT> struct Plan {
-    static constexpr bool FEW = NT <= 0;
-    static constexpr int TOK = FEW ? -NT : 8 * NT;  // tokens that sums are kept for
+    static constexpr bool ONE = NT == 0;
+    static constexpr int TOK = ONE ? 1 : 8 * NT;    // tokens that sums are kept for
     static constexpr int M = NT == 1 ? 2 : 1;       // tiles of 16 rows in a step: x is read once for them
-    static constexpr int WARPS = NT == -1 ? 24 : 16;               // at most
+    static constexpr int WARPS = ONE ? 20 : 16;                    // at most
     static constexpr int ROWS = 16 * M;
-    static constexpr int NA = M * 4 * (FEW ? TOK : NT);            // sums a lane holds
+    static constexpr int NA = M * 4 * (ONE ? 1 : NT);              // sums a lane holds
     static constexpr int SLOTS = 3;                                // of a warp's ring
     static constexpr int SLOT = ROWS * (GV_WROW + GV_SROW);
     static constexpr int WARP_BYTES = SLOTS * SLOT + NA * 32 * 4;  // shared memory of a warp
     static constexpr int fixed_bytes(int T, int K) {               // and of a block besides
-        return T * row_stride(K) + GV_ZERO + 128 + 128 + 4 * 8 * TOK * ((K + GV_COLS - 1) / GV_COLS);
+        return T * row_stride(K) + GV_ZERO + 128 + 128 + 4 * 8 * (ONE ? TOK : 2 * TOK) * ((K + GV_COLS - 1) / GV_COLS);
     }
 };
 
@@ -246,72 +245,71 @@ __device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<ROWS>& c
     }
 }
 
-// One or two tokens, M tiles of 16 rows by 256 columns: lane (g, q) reads chunk q + 4 (g & 1) of rows
-// g / 2 + 4 j. The rows g of an mma are a W row's first four groups (g even) and its last four
-// (g odd): columns 2 q, 2 q + 1 of a lane's sums count where they are that half's.
+// One token, 16 rows by 256 columns: lane (g, q) reads chunk q + 4 (g & 1) of rows g / 2 + 4 j. The
+// rows g of an mma are a W row's first four groups (g even) and its last four (g odd): columns
+// 2 q, 2 q + 1 of a lane's sums count where they are that half's.
 // w: the lane's first chunk, s: the first row's scales; `release` is called once they are read.
-// x: the lane's column of B (zeros in the lanes that hold other groups), xrow bytes from one
-// token's to the next. gs: this lane's pair of group sums, grow floats apart.
-template <int TOK, int M, class Release>
-__device__ __forceinline__ void few_step(const unsigned char* w, const unsigned char* s, Release release,
-                                         const unsigned char* x, int xrow, const float* gs, int grow,
-                                         float (&acc)[4 * M * TOK]) {
-    uint4 v[4 * M];
-    uint32_t sc[4 * M];
+// x: the lane's column of B (zeros in the lanes that hold other groups). gs: its two group sums.
+template <class Release>
+__device__ __forceinline__ void one_step(const unsigned char* w, const unsigned char* s, Release release,
+                                         const unsigned char* x, const float* gs, float (&acc)[4]) {
+    uint4 v[4];
+    uint32_t sc[4];
 #pragma unroll
-    for (int j = 0; j < 4 * M; ++j) v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * GV_WROW);
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * GV_WROW);
 #pragma unroll
-    for (int j = 0; j < 4 * M; ++j) sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * GV_SROW);
+    for (int j = 0; j < 4; ++j) sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * GV_SROW);
     release();
+    float cc[2][4];
+    const float2 c = *reinterpret_cast<const float2*>(gs);
 #pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-        float cc[2 * M][4];
-        const float2 c = *reinterpret_cast<const float2*>(gs + t * grow);
+    for (int i = 0; i < 4; ++i) {
+        const uint4 xv = *reinterpret_cast<const uint4*>(x + 16 * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(x + t * xrow + 16 * i);
-#pragma unroll
-            for (int h = 0; h < 2 * M; ++h) {
-                const uint4 va = v[2 * h], vb = v[2 * h + 1];
-                const uint32_t a = i == 0 ? va.x : i == 1 ? va.y : i == 2 ? va.z : va.w;
-                const uint32_t b = i == 0 ? vb.x : i == 1 ? vb.y : i == 2 ? vb.z : vb.w;
-                float(&d)[4] = cc[h];
-                if (i == 0) mma_word(d, a, b, xv, c.x, c.y, c.x, c.y);
-                else mma_word(d, a, b, xv, d[0], d[1], d[2], d[3]);
-            }
+        for (int h = 0; h < 2; ++h) {
+            const uint4 va = v[2 * h], vb = v[2 * h + 1];
+            const uint32_t a = i == 0 ? va.x : i == 1 ? va.y : i == 2 ? va.z : va.w;
+            const uint32_t b = i == 0 ? vb.x : i == 1 ? vb.y : i == 2 ? vb.z : vb.w;
+            float(&d)[4] = cc[h];
+            if (i == 0) mma_word(d, a, b, xv, c.x, c.y, c.x, c.y);
+            else mma_word(d, a, b, xv, d[0], d[1], d[2], d[3]);
         }
+    }
 #pragma unroll
-        for (int j = 0; j < 4 * M; ++j) {
-            const int k = 4 * M * t + j, e = 2 * (j & 1);
-            acc[k] = fmaf(cc[j / 2][e], bf16lo(sc[j]), fmaf(cc[j / 2][e + 1], bf16hi(sc[j]), acc[k]));
-        }
+    for (int j = 0; j < 4; ++j) {
+        const int e = 2 * (j & 1);
+        acc[j] = fmaf(cc[j / 2][e], bf16lo(sc[j]), fmaf(cc[j / 2][e + 1], bf16hi(sc[j]), acc[j]));
     }
 }
 
 // Eight NT tokens, M tiles of 16 rows by 128 columns: lane (g, q) reads its quarter of the four
 // groups of rows g and g + 8; x holds the lane's token of each block of eight, gs the group sums
-// of the lane's two tokens of C in the first block.
-template <int NT, int M>
-__device__ __forceinline__ void row_step(const unsigned char* w, const unsigned char* s, const unsigned char* const (&x)[NT],
-                                         const float* gs, float (&acc)[4 * NT * M]) {
+// that the lane's part of C starts with in the first block.
+template <int NT, int M, class Release>
+__device__ __forceinline__ void row_step(const unsigned char* w, const unsigned char* s, Release release,
+                                         const unsigned char* const (&x)[NT], const float* gs, float (&acc)[4 * NT * M]) {
     uint2 sc[2 * M];
+    uint32_t w4[4][2 * M];
 #pragma unroll
     for (int m = 0; m < 2 * M; ++m) sc[m] = *reinterpret_cast<const uint2*>(s + 8 * m * GV_SROW);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t v[2 * M];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int m = 0; m < 2 * M; ++m) v[m] = *reinterpret_cast<const uint32_t*>(w + 8 * m * GV_WROW + 16 * i);
+        for (int m = 0; m < 2 * M; ++m) w4[i][m] = *reinterpret_cast<const uint32_t*>(w + 8 * m * GV_WROW + 16 * i);
+    release();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t(&v)[2 * M] = w4[i];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const uint4 xv = *reinterpret_cast<const uint4*>(x[nt] + 64 * i);
-            const float2 c = *reinterpret_cast<const float2*>(gs + i * (8 * NT) + 8 * nt);
+            const float4 c = *reinterpret_cast<const float4*>(gs + i * (16 * NT) + 16 * nt);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const uint32_t ua = i < 2 ? sc[2 * m].x : sc[2 * m].y, ub = i < 2 ? sc[2 * m + 1].x : sc[2 * m + 1].y;
                 const float fa = i & 1 ? bf16hi(ua) : bf16lo(ua), fb = i & 1 ? bf16hi(ub) : bf16lo(ub);
                 float cc[4];
-                mma_word(cc, v[2 * m], v[2 * m + 1], xv, c.x, c.y, c.x, c.y);
+                mma_word(cc, v[2 * m], v[2 * m + 1], xv, c.x, c.y, c.z, c.w);
                 float* to = acc + 4 * (m * NT + nt);
                 const float2 u = __ffma2_rn(make_float2(cc[0], cc[1]), make_float2(fa, fa), make_float2(to[0], to[1]));
                 const float2 v2 = __ffma2_rn(make_float2(cc[2], cc[3]), make_float2(fb, fb), make_float2(to[2], to[3]));
@@ -327,12 +325,12 @@ __device__ __forceinline__ void put(void* y, size_t i, float v) {
     else static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
 }
 
-// NT < 0: -NT tokens (one or two); otherwise NT blocks of eight. All of x in shared memory.
+// NT = 0: one token; otherwise NT blocks of eight. All of x in shared memory.
 template <int NT, bool F32, bool WHOLE>
 __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const GemvParams p) {
     extern __shared__ __align__(16) unsigned char sm[];
     using P = Plan<NT>;
-    constexpr bool FEW = P::FEW;
+    constexpr bool ONE = P::ONE;
     constexpr int TOK = P::TOK, NA = P::NA, ROWS = P::ROWS, RING = P::SLOTS * P::SLOT;
     const int steps = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -340,8 +338,8 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     unsigned char* xs = sm;
     unsigned char* zero = xs + size_t(p.T) * stride;
     int* exps = reinterpret_cast<int*>(zero + GV_ZERO);     // [TOK], in 128 bytes
-    float* gsum = reinterpret_cast<float*>(exps + 32);      // [TOK][8 steps] or [8 steps][TOK]
-    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + TOK * 8 * steps);  // 128 bytes
+    float* gsum = reinterpret_cast<float*>(exps + 32);      // [TOK][8 steps] or [8 steps][2 TOK]
+    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + (ONE ? 1 : 2) * TOK * 8 * steps);  // 128 bytes
     float* red = reinterpret_cast<float*>(tops + 32);                      // [warps][NA][32]
     unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * RING;
 
@@ -371,33 +369,27 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     for (int i = 0; i < P::SLOTS - 1; ++i) ask();
     if (threadIdx.x < GV_ZERO / 16) reinterpret_cast<uint4*>(zero)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     cp_wait<P::SLOTS - 1>();
-    shape_x<FEW, TOK>(p, share, stride, xs, zero, gsum, exps, tops);
+    shape_x<ONE, TOK>(p, share, stride, xs, zero, gsum, exps, tops);
 
-    const int xrow = FEW && (g & 3) == q ? stride : 0;
-    constexpr int NX = FEW ? 1 : NT;
+    constexpr int NX = ONE ? 1 : NT;
     const unsigned char* x0[NX];
     int xstep[NX];  // bytes a step adds
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-        const bool there = FEW ? (g & 3) == q : 8 * i + g < p.T;  // few tokens: this lane is its column's group
-        x0[i] = (there ? xs + (FEW ? 64 * g : (8 * i + g) * stride) : zero) + (FEW ? 0 : 16 * q);
+        const bool there = ONE ? (g & 3) == q : 8 * i + g < p.T;  // one token: this lane is its column's group
+        x0[i] = (there ? xs + (ONE ? 64 * g : (8 * i + g) * stride) : zero) + (ONE ? 0 : 16 * q);
         xstep[i] = there ? 2 * GV_COLS : 0;
     }
-    const unsigned char* my_w = ring + (FEW ? (lane / 8) * GV_WROW + 16 * (lane % 8) : g * GV_WROW + 4 * q);
-    const unsigned char* my_s = ring + ROWS * GV_WROW + (FEW ? (lane / 8) * GV_SROW + 4 * q : g * GV_SROW);
-    const float* my_g = gsum + 2 * q;
+    const unsigned char* my_w = ring + (ONE ? (lane / 8) * GV_WROW + 16 * (lane % 8) : g * GV_WROW + 4 * q);
+    const unsigned char* my_s = ring + ROWS * GV_WROW + (ONE ? (lane / 8) * GV_SROW + 4 * q : g * GV_SROW);
+    const float* my_g = gsum + (ONE ? 2 : 4) * q;
 
     float acc[NA] = {};
     auto put_tile = [&](int tl, const float (&v)[NA]) {
-        if constexpr (FEW) {  // the sums are in all eight lanes of a row: lane m stores sum m of each token
+        if constexpr (ONE) {  // the sums are in all eight lanes of a row: lane m stores sum m
             const int m = lane % 8, n = tl * ROWS + lane / 8 + 4 * m;
-#pragma unroll
-            for (int t = 0; t < TOK; ++t) {
-                float u = v[4 * P::M * t];
-#pragma unroll
-                for (int i = 1; i < 4 * P::M; ++i) u = m == i ? v[4 * P::M * t + i] : u;
-                if (m < 4 * P::M && n < p.N) put<F32>(p.y, size_t(t) * p.N + n, ldexpf(u, exps[t] + 133 - GV_TOP));
-            }
+            const float u = m == 0 ? v[0] : m == 1 ? v[1] : m == 2 ? v[2] : v[3];
+            if (m < 4 && n < p.N) put<F32>(p.y, n, ldexpf(u, exps[0] + 133 - GV_TOP));
         } else {
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
@@ -408,7 +400,7 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     };
     bool whole = s == 0;  // the segment at hand starts at its tile's first step
     auto finish = [&](bool ended) {
-        if constexpr (FEW) {  // add the four lanes that hold the row's groups; the other four hold none of it
+        if constexpr (ONE) {  // add the four lanes that hold the row's groups; the other four hold none of it
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
                 float v = (q >> 1) == (g & 1) ? acc[i] : 0.0f;
@@ -432,17 +424,16 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
             __syncwarp();  // the slot has been read
             ask();
         };
-        if constexpr (FEW) {
-            few_step<TOK, P::M>(w, sc, release, x0[0] + s * xstep[0], xrow, my_g + 8 * s, 8 * steps, acc);
+        if constexpr (ONE) {
+            one_step(w, sc, release, x0[0] + s * xstep[0], my_g + 8 * s, acc);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const unsigned char* xp[NX];
 #pragma unroll
                 for (int i = 0; i < NX; ++i) xp[i] = x0[i] + s * xstep[i] + h * (xstep[i] / 2);
-                row_step<NT, P::M>(w + 64 * h, sc + 8 * h, xp, my_g + (8 * s + 4 * h) * TOK, acc);
+                row_step<NT, P::M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * (2 * TOK), acc);
             }
-            release();
         }
         slot = slot + P::SLOT == RING ? 0 : slot + P::SLOT;
         if (++s == steps) {
@@ -491,9 +482,8 @@ bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
 
 // Whether T tokens of K columns leave room for eight warps' rings.
 bool fits(int T, int K, int smem) {
-    const int need = T == 1   ? Plan<-1>::fixed_bytes(T, K) + 8 * Plan<-1>::WARP_BYTES
-                     : T == 2 ? Plan<-2>::fixed_bytes(T, K) + 8 * Plan<-2>::WARP_BYTES
-                     : T <= 8 ? Plan<1>::fixed_bytes(T, K) + 8 * Plan<1>::WARP_BYTES
+    const int need = T == 1    ? Plan<0>::fixed_bytes(T, K) + 8 * Plan<0>::WARP_BYTES
+                     : T <= 8  ? Plan<1>::fixed_bytes(T, K) + 8 * Plan<1>::WARP_BYTES
                      : T <= 16 ? Plan<2>::fixed_bytes(T, K) + 8 * Plan<2>::WARP_BYTES
                                : Plan<4>::fixed_bytes(T, K) + 8 * Plan<4>::WARP_BYTES;
     return need <= smem;
@@ -501,8 +491,7 @@ bool fits(int T, int K, int smem) {
 
 template <bool F32, bool WHOLE>
 bool launch_tokens(const GemvParams& p, const DevInfo& di, cudaStream_t s) {
-    if (p.T == 1) return launch_gemv<-1, F32, WHOLE>(p, di, s);
-    if (p.T == 2) return launch_gemv<-2, F32, WHOLE>(p, di, s);
+    if (p.T == 1) return launch_gemv<0, F32, WHOLE>(p, di, s);
     if (p.T <= 8) return launch_gemv<1, F32, WHOLE>(p, di, s);
     if (p.T <= 16) return launch_gemv<2, F32, WHOLE>(p, di, s);
     return launch_gemv<4, F32, WHOLE>(p, di, s);

@@ -46,7 +46,8 @@ struct NormParams {
     void *h_out, *x;       // forward outputs
     const void *dh_out, *dx;
     void *dh, *dy, *dgate;
-    float* part;  // backward: [blocks][3][H] column sums (pre_w, post_w, channel gate)
+    float* part;  // backward: [blocks][2][H] column sums: dpre_w and A
+    int units, ahead;  // walked rows: 16-byte units of a chunk, rows in flight (0 .. 2)
     bool want_pre, want_post, want_gate;
 };
 
@@ -54,348 +55,460 @@ struct NormParams {
 // memory in warp order. `buf` alternates between two areas from call to call, so that one
 // barrier a call is enough: an area is written again only behind the barrier of the call
 // between, which every thread reaches after its reads.
+constexpr int RED = 3 * 16;  // floats of an area: up to three sums of up to 16 warps a group
+
+// Warp sums of two or three values, two lanes' worth at a time: the halves of the warp exchange and
+// keep different values, so the later steps carry fewer. Afterwards lane 0 has v[0], lane 8 v[1] and
+// lane 16 v[2] (N = 3), or lane 0 v[0] and lane 16 v[1] (N = 2); returns this lane's.
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&v)[N]) {
+    const bool high = threadIdx.x & 16, mid = threadIdx.x & 8;
+    float a;
+    if constexpr (N == 1) {
+        a = v[0] + __shfl_xor_sync(FULL, v[0], 16);
+        a += __shfl_xor_sync(FULL, a, 8);
+    } else if constexpr (N == 2) {
+        a = (high ? v[1] : v[0]) + __shfl_xor_sync(FULL, high ? v[0] : v[1], 16);
+        a += __shfl_xor_sync(FULL, a, 8);
+    } else {
+        a = (high ? v[2] : v[0]) + __shfl_xor_sync(FULL, high ? v[0] : v[2], 16);
+        const float b = v[1] + __shfl_xor_sync(FULL, v[1], 16);
+        // lower half: keep v[0] or v[1] by the bit of 8; upper half: v[2] in both
+        const float keep = !high && mid ? b : a, give = !high && !mid ? b : a;
+        a = keep + __shfl_xor_sync(FULL, give, 8);
+    }
+    a += __shfl_xor_sync(FULL, a, 4);
+    a += __shfl_xor_sync(FULL, a, 2);
+    return a + __shfl_xor_sync(FULL, a, 1);
+}
+
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int tpr, int group, int wig) {
+    const float a = warp_sums<N>(v);
+    const int l = threadIdx.x & 31;
+    const int which = N == 1 ? (l == 0 ? 0 : -1) : N == 2 ? (l == 0 ? 0 : l == 16 ? 1 : -1)
+                                                          : (l == 0 ? 0 : l == 8 ? 1 : l == 16 ? 2 : -1);
+    if (tpr == 32) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (tpr == 32) return;
-    const int nw = tpr / 32;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) buf[wig * N + i] = v[i];
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(FULL, a, N == 3 ? 8 * i : 16 * i);
+        return;
     }
+    if (which >= 0) buf[which * 16 + wig] = a;
     asm volatile("bar.sync %0, %1;" :: "r"(group + 1), "r"(tpr) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    for (int w = 0; w < nw; ++w) {
+    for (int w = 0; w < tpr / 32; w += 4) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += buf[w * N + i];
+        for (int i = 0; i < N; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(buf + i * 16 + w);  // zeros behind the last warp
+            v[i] += (f.x + f.y) + (f.z + f.w);
+        }
     }
 }
 
-__device__ __forceinline__ float sigmoid(float a) { return 1.0f / (1.0f + expf(-a)); }
-
-__device__ __forceinline__ void gate8(const NormParams& p, int t, int c, float (&g)[8]) {
-    if (p.gate_kind == GATE_ELEMENT) {
-        load8_shared(p.gate, p.gate_f32, size_t(t) * p.chunks + c, g);
-    } else if (p.gate_kind == GATE_CHANNEL) {
-        load8_shared(p.gate, p.gate_f32, c, g);
-    } else {
-        const float v = load1(p.gate, p.gate_f32, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = v;
-    }
+// The places of warps that a group does not have, read as zeros by group_sum (whose barrier
+// publishes them).
+__device__ __forceinline__ void clear_unused(float* a, float* b, int lane, int tpr) {
+    for (int i = lane; i < RED; i += tpr)
+        if (i % 16 >= tpr / 32) a[i] = b[i] = 0.0f;
 }
 
-// One row per group of p.tpr threads; NC chunks a thread (chunk c = thread + i tpr).
+// 1 / (1 + e^-a). The fast exponential is off by about 2 + 1.2 |a| units of e^-a, so by that much
+// only where e^-a decides (a < 0), 3 units in all at |a| = 1 and 14 at a = -10; the accurate one
+// and an IEEE divide cost 20 instructions more an element (the wide gated case: 134 against 96 us
+// together with packed arithmetic).
+__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
+__device__ __forceinline__ F8 sigmoid(const F8& a) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = make_float2(sigmoid(a.v[i].x), sigmoid(a.v[i].y));
+    return r;
+}
+
+// One row per group of p.tpr threads; NC chunks a thread (chunk c = thread + i tpr). Everything a
+// row needs is asked for before the first sum waits.
 template <int HD, int YD, int XD, int NC, bool BRANCH>
-__global__ void __launch_bounds__(512) norm_forward_kernel(const NormParams p) {
-    __shared__ float red[2][32];
+__global__ void __launch_bounds__(512, 2) norm_forward_kernel(const NormParams p) {
+    constexpr bool EARLY = NC == 1;  // the weights too, where registers allow
+    __shared__ __align__(16) float red[2][8][RED];
     const int group = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr, wig = lane / 32;
     const int rows = blockDim.x / p.tpr;
     const long long t = (long long)blockIdx.x * rows + group;
     if (t >= p.T) return;  // whole groups only: the group barriers stay complete
-    const int wbase = group * (p.tpr / 32);
     const size_t row = size_t(t) * p.chunks;
+    clear_unused(red[0][group], red[1][group], lane, p.tpr);
 
     Raw8<HD> hr[NC];
     Raw8<YD> yr[NC];
+    RawAny w1[NC], w2[NC], gr[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = lane + i * p.tpr;
-        if (c < p.chunks) {
-            if (BRANCH) yr[i].load(p.y, row + c);
-            hr[i].load(p.h, row + c);
-        } else {
-            if (BRANCH) yr[i].zero();
-            hr[i].zero();
-        }
+        hr[i].zero();
+        if (BRANCH) yr[i].zero();
+        if (c >= p.chunks) continue;
+        if (BRANCH) yr[i].load(p.y, row + c);
+        hr[i].load(p.h, row + c);
+        if (BRANCH && p.gate_kind >= GATE_CHANNEL)
+            gr[i].load(p.gate, p.gate_f32, p.gate_kind == GATE_ELEMENT ? row + c : size_t(c));
+        if (EARLY && BRANCH && p.post_w) w1[i].load(p.post_w, p.w_f32, c);
+        if (EARLY && p.x && p.pre_w) w2[i].load(p.pre_w, p.w_f32, c);
     }
-    float h[NC][8];
+    float token = 1.0f;
+    if (BRANCH && p.gate_kind == GATE_TOKEN) {
+        token = load1(p.gate, p.gate_f32, t);
+        if (p.sigmoid) token = sigmoid(token);
+    }
+    F8 h[NC];
     if (BRANCH) {
-        float y[NC][8];
-        float r1 = 1.0f;
+        F8 y[NC];
+        float scale = p.block_scale * token;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) yr[i].get(y[i]);
+        for (int i = 0; i < NC; ++i) y[i] = yr[i].get();
         if (p.post_norm) {
-            float s[1] = {0.0f};
+            float2 q = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[0] = fmaf(y[i][j], y[i][j], s[0]);
-            group_sum<1>(s, red[0] + wbase, p.tpr, group, wig);
-            r1 = rsqrtf(fmaf(s[0], p.inv_h, p.eps));
+            for (int i = 0; i < NC; ++i) dot(y[i], y[i], q);
+            float s[1] = {q.x + q.y};
+            group_sum<1>(s, red[0][group], p.tpr, group, wig);
+            scale *= rsqrtf(fmaf(s[0], p.inv_h, p.eps));
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
-            hr[i].get(h[i]);
+            h[i] = hr[i].get();
             if (c >= p.chunks) continue;
-            float u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = y[i][j] * r1;
-            if (p.post_norm && p.post_w) {
-                float w[8];
-                load8_shared(p.post_w, p.w_f32, c, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] *= p.w_offset + w[j];
+            if (p.post_w) {
+                if (!EARLY) w1[i].load(p.post_w, p.w_f32, c);
+                y[i] = mul(y[i], add(w1[i].get(p.w_f32), p.w_offset));
             }
-            if (p.gate_kind != GATE_NONE) {
-                float g[8];
-                gate8(p, int(t), c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] *= p.sigmoid ? sigmoid(g[j]) : g[j];
+            if (p.gate_kind >= GATE_CHANNEL) {
+                const F8 g = gr[i].get(p.gate_f32);
+                y[i] = mul(y[i], p.sigmoid ? sigmoid(g) : g);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = fmaf(p.res_scale, h[i][j], p.block_scale * u[j]);
+            h[i] = fma(y[i], scale, mul(h[i], p.res_scale));
             store8<HD>(p.h_out, row + c, h[i]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) hr[i].get(h[i]);
+        for (int i = 0; i < NC; ++i) h[i] = hr[i].get();
     }
     if (!p.x) return;
-    float s[1] = {0.0f};
+    float2 q = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);  // zero beyond the row
-    group_sum<1>(s, red[1] + wbase, p.tpr, group, wig);
+    for (int i = 0; i < NC; ++i) dot(h[i], h[i], q);  // zero beyond the row
+    float s[1] = {q.x + q.y};
+    group_sum<1>(s, red[1][group], p.tpr, group, wig);
     const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = lane + i * p.tpr;
         if (c >= p.chunks) continue;
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = h[i][j] * r2;
+        F8 x = mul(h[i], r2);
         if (p.pre_w) {
-            float w[8];
-            load8_shared(p.pre_w, p.w_f32, c, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= p.w_offset + w[j];
+            if (!EARLY) w2[i].load(p.pre_w, p.w_f32, c);
+            x = mul(x, add(w2[i].get(p.w_f32), p.w_offset));
         }
         store8<XD>(p.x, row + c, x);
     }
 }
 
-// Backward: each group walks rows blockIdx * rows + group, + gridDim * rows, ... and keeps the
-// column sums of its rows in registers; the block adds its groups' sums in order and stores
-// one partial row per weight, which norm_columns_kernel adds over the blocks.
-template <int HD, int YD, int XD, int NC, bool BRANCH>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p) {
-    extern __shared__ __align__(16) float cols[];  // [groups - 1][3][chunks * 8] where groups > 1
-    __shared__ float red[2][3 * 32];
+// ---- long batches: blocks that stay and walk rows, the next rows in flight ----
+//
+// A thread copies its own 16-byte units of the rows ahead into shared memory, asynchronously, and
+// reads only those: a row's arrival needs no barrier, and what is in flight needs no registers.
+// What all rows share is combined once per block into two fp32 vectors in shared memory:
+//   pre[c]  = w_offset + pre_w                              (1 without weights)
+//   post[c] = block_scale act(gate) (w_offset + post_w)     (no or channel gate)
+//             w_offset + post_w                             (token or element gate)
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+template <int U>
+__device__ __forceinline__ F8 lds8(uint32_t at, int stride) {  // one chunk of U units
+    const uint4 a = lds16(at);
+    if constexpr (U == 2) return f32x8(a, lds16(at + stride));
+    else return bf16x8(a);
+}
+__device__ __forceinline__ F8 lds8f(uint32_t at) { return f32x8(lds16(at), lds16(at + 16)); }
+
+template <int U>
+__device__ __forceinline__ void copy_units(uint32_t dst, int stride, const void* p, size_t chunk) {
+    const uint4* src = static_cast<const uint4*>(p) + U * chunk;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst + i * stride), "l"(src + i) : "memory");
+}
+__device__ __forceinline__ void copy_gate(const NormParams& p, uint32_t dst, int stride, size_t chunk) {
+    if (p.gate_f32) copy_units<2>(dst, stride, p.gate, chunk);
+    else copy_units<1>(dst, stride, p.gate, chunk);
+}
+__device__ __forceinline__ void rows_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void rows_wait(int ahead) {  // all but the `ahead` newest
+    if (ahead == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ void shared_vectors(const NormParams& p, bool branch, float* post, float* pre) {
+    for (int c = threadIdx.x; c < p.chunks; c += blockDim.x) {
+        RawAny a, b, g;
+        if (p.pre_w) a.load(p.pre_w, p.w_f32, c);
+        if (p.post_w) b.load(p.post_w, p.w_f32, c);
+        const bool channel = branch && p.gate_kind == GATE_CHANNEL;
+        if (channel) g.load(p.gate, p.gate_f32, c);
+        store8<DT_F32>(pre, c, p.pre_w ? add(a.get(p.w_f32), p.w_offset) : fill8(1.0f));
+        F8 v = p.post_w ? add(b.get(p.w_f32), p.w_offset) : fill8(1.0f);
+        if (channel) {
+            const F8 w = g.get(p.gate_f32);
+            v = mul(v, p.sigmoid ? sigmoid(w) : w);
+        }
+        if (channel || (branch && p.gate_kind == GATE_NONE)) v = mul(v, p.block_scale);
+        store8<DT_F32>(post, c, v);
+    }
+}
+
+// Backward. Without an element or token gate, the gradients of post_w and of a channel gate are
+// per-column multiples of one sum, A = sum_t G y r1: norm_columns_kernel makes both from it. With
+// them A takes each row's gate in and is dpost_w itself.
+template <int HD, int YD, int XD, int NC, bool BRANCH, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward_kernel(const NormParams p) {
+    constexpr int UH = HD == DT_F32 ? 2 : 1, UX = XD == DT_F32 ? 2 : 1, UY = BRANCH ? (YD == DT_F32 ? 2 : 1) : 0;
+    constexpr int AT_G = UH, AT_X = 2 * UH, AT_Y = AT_X + UX, AT_GATE = AT_Y + UY;  // units: h_out, dh_out, dx, y, gate
+    extern __shared__ __align__(16) float dyn[];  // post, pre [H] each, then the rows' units; at the end
+                                                  // the column sums [groups - 1][2][H]
+    __shared__ __align__(16) float red[2][8][RED];
     const int group = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr, wig = lane / 32;
     const int rows = blockDim.x / p.tpr;
-    const int wbase = group * (p.tpr / 32);
-    int turn = 0;
-    float acc_pre[NC][8] = {}, acc_post[NC][8] = {}, acc_gate[NC][8] = {};
+    clear_unused(red[0][group], red[1][group], lane, p.tpr);
+    const int stride = blockDim.x * 16, chunk_bytes = p.units * stride, stage_bytes = NC * chunk_bytes;
+    const uint32_t post = smem_u32(dyn), pre = post + 4 * p.H, mine = pre + 4 * p.H + 16 * threadIdx.x;
+    const bool has_x = p.dx != nullptr, has_g = p.dh_out != nullptr, post_norm = BRANCH && p.post_norm,
+               element = BRANCH && p.gate_kind == GATE_ELEMENT, tokens = BRANCH && p.gate_kind == GATE_TOKEN;
+    const long long step = (long long)gridDim.x * rows;
+    long long t = (long long)blockIdx.x * rows + group;
+    int in = 0, use = 0;
+    auto ask = [&](long long r) {
+        if (r < p.T) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = lane + i * p.tpr;
+                if (c >= p.chunks) continue;
+                const size_t k = size_t(r) * p.chunks + c;
+                const uint32_t d = mine + in * stage_bytes + i * chunk_bytes;
+                copy_units<UH>(d, stride, p.h, k);
+                if (has_g) copy_units<UH>(d + AT_G * stride, stride, p.dh_out, k);
+                if (has_x) copy_units<UX>(d + AT_X * stride, stride, p.dx, k);
+                if constexpr (BRANCH) copy_units<UY>(d + AT_Y * stride, stride, p.y, k);
+                if (element) copy_gate(p, d + AT_GATE * stride, stride, k);
+            }
+        }
+        in = in == p.ahead ? 0 : in + 1;
+        rows_commit();
+    };
+    for (int i = 0; i < p.ahead; ++i) ask(t + i * step);
+    shared_vectors(p, BRANCH, dyn, dyn + p.H);
+    __syncthreads();
 
-    for (long long t = (long long)blockIdx.x * rows + group; t < p.T; t += (long long)gridDim.x * rows) {
+    int turn = 0;
+    F8 acc_pre[NC], acc_post[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) acc_pre[i] = acc_post[i] = fill8(0.0f);
+    for (; t < p.T; t += step) {
         const size_t row = size_t(t) * p.chunks;
-        Raw8<HD> hr[NC], gr[NC];
-        Raw8<YD> yr[NC];
-        Raw8<XD> xr[NC];
+        float token = 1.0f, dtoken = 1.0f;
+        if (tokens) {
+            token = load1(p.gate, p.gate_f32, t);
+            if (p.sigmoid) {
+                token = sigmoid(token);
+                dtoken = token * (1.0f - token);
+            }
+        }
+        ask(t + p.ahead * step);
+        rows_wait(p.ahead);
+        const uint32_t at = mine + use * stage_bytes;
+        use = use == p.ahead ? 0 : use + 1;
+
+        // a thread's one chunk stays in registers between the sums; two would not fit beside the
+        // column sums and are read again
+        F8 h, a, y;
+        auto read = [&](uint32_t u) {
+            h = lds8<UH>(u, stride);
+            if (has_x) a = lds8<UX>(u + AT_X * stride, stride);
+            if constexpr (BRANCH) y = lds8<UY>(u + AT_Y * stride, stride);
+        };
+        float2 q0 = both(0.0f), q1 = q0, q2 = q0;  // h_out^2, dx pre h_out, y^2
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
-            const bool in = c < p.chunks;
-            hr[i].zero(); gr[i].zero(); xr[i].zero(); yr[i].zero();
-            if (in) hr[i].load(p.h, row + c);
-            if (in && p.dx) xr[i].load(p.dx, row + c);
-            if (in && p.dh_out) gr[i].load(p.dh_out, row + c);
-            if (BRANCH && in) yr[i].load(p.y, row + c);
-        }
-        float h[NC][8], G[NC][8], y[NC][8];
-        float s[3] = {0.0f, 0.0f, 0.0f};  // h_out^2, dx w2 h_out, y^2
-        float a[NC][8];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            hr[i].get(h[i]);
-            xr[i].get(a[i]);
-            if (BRANCH) yr[i].get(y[i]);
-            float w[8];
-            if (p.dx && p.pre_w && c < p.chunks) {
-                load8_shared(p.pre_w, p.w_f32, c, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] += p.w_offset;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+            if (c >= p.chunks) continue;
+            read(at + i * chunk_bytes);
+            if (has_x) {
+                dot(h, h, q0);
+                dot(mul(a, lds8f(pre + 32 * c)), h, q1);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[0] = fmaf(h[i][j], h[i][j], s[0]);
-                s[1] = fmaf(a[i][j] * w[j], h[i][j], s[1]);
-                if (BRANCH) s[2] = fmaf(y[i][j], y[i][j], s[2]);
-                G[i][j] = a[i][j] * w[j];
-            }
+            if (BRANCH) dot(y, y, q2);
         }
-        group_sum<3>(s, red[turn] + 3 * wbase, p.tpr, group, wig);
+        float s[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
+        group_sum<3>(s, red[turn][group], p.tpr, group, wig);
         turn ^= 1;
         const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps));
         const float k2 = r2 * r2 * (s[1] * p.inv_h);
-        const float r1 = BRANCH && p.post_norm ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.0f;
-        float q[2] = {0.0f, 0.0f};  // d w1 y, and the token gate's b u
+        const float r1 = post_norm ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.0f;
+        q0 = q1 = both(0.0f);  // c y, and the token gate's b u
+        F8 G[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
             if (c >= p.chunks) continue;
-            float dho[8], dh[8];
-            gr[i].get(dho);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (p.dx) {
-                    acc_pre[i][j] = fmaf(a[i][j] * r2, h[i][j], acc_pre[i][j]);
-                    G[i][j] = fmaf(r2, G[i][j] - h[i][j] * k2, dho[j]);
-                } else {
-                    G[i][j] = dho[j];
-                }
-                dh[j] = BRANCH ? p.res_scale * G[i][j] : G[i][j];
+            const uint32_t u = at + i * chunk_bytes;
+            if (NC > 1) read(u);
+            if (has_g) G[i] = lds8<UH>(u + AT_G * stride, stride);
+            else G[i] = fill8(0.0f);
+            if (has_x) {
+                acc_pre[i] = fma(a, mul(h, r2), acc_pre[i]);
+                G[i] = fma(fma(h, -k2, mul(a, lds8f(pre + 32 * c))), r2, G[i]);
             }
-            store8<HD>(p.dh, row + c, dh);
-            if (!BRANCH) continue;
-            float w1[8];
-            if (p.post_norm && p.post_w) {
-                load8_shared(p.post_w, p.w_f32, c, w1);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w1[j] += p.w_offset;
+            if constexpr (!BRANCH) {
+                store8<HD>(p.dh, row + c, G[i]);
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w1[j] = 1.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) G[i][j] *= p.block_scale;  // b
-            if (p.gate_kind != GATE_NONE) {
-                float g[8], dg[8];
-                gate8(p, int(t), c, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v = g[j], dv = 1.0f;
+                store8<HD>(p.dh, row + c, mul(G[i], p.res_scale));
+                const F8 yn = mul(y, r1), w = lds8f(post + 32 * c);
+                if (element) {
+                    F8 v = p.gate_f32 ? lds8<2>(u + AT_GATE * stride, stride) : lds8<1>(u + AT_GATE * stride, stride);
+                    G[i] = mul(G[i], p.block_scale);
+                    F8 dg = mul(mul(G[i], yn), w);
                     if (p.sigmoid) {
                         v = sigmoid(v);
-                        dv = v * (1.0f - v);
+                        dg = mul(dg, fma(mul(v, -1.0f), v, v));  // v (1 - v)
                     }
-                    dg[j] = G[i][j] * (y[i][j] * r1 * w1[j]) * dv;
-                    G[i][j] *= v;  // d
-                    q[1] += dg[j];
-                    if (p.gate_kind == GATE_CHANNEL) acc_gate[i][j] += dg[j];
+                    if (p.dgate) {
+                        if (p.gate_f32) store8<DT_F32>(p.dgate, row + c, dg);
+                        else store8<DT_BF16>(p.dgate, row + c, dg);
+                    }
+                    G[i] = mul(G[i], v);
+                } else if (tokens) {
+                    G[i] = mul(G[i], p.block_scale);
+                    dot(mul(G[i], yn), w, q1);
+                    G[i] = mul(G[i], token);
                 }
-                if (p.gate_kind == GATE_ELEMENT && p.dgate) {
-                    if (p.gate_f32) store8<DT_F32>(p.dgate, row + c, dg);
-                    else store8<DT_BF16>(p.dgate, row + c, dg);
-                }
-            }
-            if (p.post_norm) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    acc_post[i][j] = fmaf(G[i][j] * r1, y[i][j], acc_post[i][j]);
-                    G[i][j] *= w1[j];  // c
-                    q[0] = fmaf(G[i][j], y[i][j], q[0]);
-                }
-            } else {
-                store8<YD>(p.dy, row + c, G[i]);
+                acc_post[i] = fma(G[i], yn, acc_post[i]);
+                G[i] = mul(G[i], w);  // c, or dy where y is not normalised
+                if (post_norm) dot(G[i], y, q0);
+                else store8<YD>(p.dy, row + c, G[i]);
             }
         }
-        if (!BRANCH || !(p.post_norm || p.gate_kind == GATE_TOKEN)) continue;
-        group_sum<2>(q, red[turn] + 3 * wbase, p.tpr, group, wig);
+        if (!post_norm && !tokens) continue;
+        float u[2] = {q0.x + q0.y, q1.x + q1.y};
+        group_sum<2>(u, red[turn][group], p.tpr, group, wig);
         turn ^= 1;
-        if (p.gate_kind == GATE_TOKEN && p.dgate && lane == 0) static_cast<float*>(p.dgate)[t] = q[1];
-        if (!p.post_norm) continue;
-        const float k1 = r1 * r1 * (q[0] * p.inv_h);
+        if (tokens && p.dgate && lane == 0) static_cast<float*>(p.dgate)[t] = u[1] * dtoken;
+        if (!post_norm) continue;
+        const float k1 = r1 * r1 * (u[0] * p.inv_h);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
             if (c >= p.chunks) continue;
-            float dy[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dy[j] = r1 * (G[i][j] - y[i][j] * k1);
-            store8<YD>(p.dy, row + c, dy);
+            if constexpr (BRANCH && NC > 1) y = lds8<UY>(at + i * chunk_bytes + AT_Y * stride, stride);
+            store8<YD>(p.dy, row + c, mul(fma(y, -k1, G[i]), r1));
         }
     }
     if (!p.part) return;
     // the groups' column sums, added in group order by group 0
+    __syncthreads();
     if (group > 0) {
-        float* m = cols + size_t(group - 1) * 3 * p.H;
+        float* m = dyn + size_t(group - 1) * 2 * p.H;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
             if (c >= p.chunks) continue;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                m[c * 8 + j] = acc_pre[i][j];
-                m[p.H + c * 8 + j] = acc_post[i][j];
-                m[2 * p.H + c * 8 + j] = acc_gate[i][j];
-            }
+            store8<DT_F32>(m, c, acc_pre[i]);
+            store8<DT_F32>(m + p.H, c, acc_post[i]);
         }
     }
     __syncthreads();
     if (group > 0) return;
-    float* out = p.part + size_t(blockIdx.x) * 3 * p.H;
+    float* out = p.part + size_t(blockIdx.x) * 2 * p.H;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = lane + i * p.tpr;
         if (c >= p.chunks) continue;
         for (int g = 0; g + 1 < rows; ++g) {
-            const float* m = cols + size_t(g) * 3 * p.H;
+            const uint32_t m = post + 4 * (g * 2 * p.H + 8 * c);
+            const F8 u = lds8f(m), v = lds8f(m + 4 * p.H);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc_pre[i][j] += m[c * 8 + j];
-                acc_post[i][j] += m[p.H + c * 8 + j];
-                acc_gate[i][j] += m[2 * p.H + c * 8 + j];
+            for (int j = 0; j < 4; ++j) {
+                acc_pre[i].v[j] = __fadd2_rn(acc_pre[i].v[j], u.v[j]);
+                acc_post[i].v[j] = __fadd2_rn(acc_post[i].v[j], v.v[j]);
             }
         }
         if (p.want_pre) store8<DT_F32>(out, c, acc_pre[i]);
-        if (p.want_post) store8<DT_F32>(out + p.H, c, acc_post[i]);
-        if (p.want_gate) store8<DT_F32>(out + 2 * p.H, c, acc_gate[i]);
+        if (p.want_post || p.want_gate) store8<DT_F32>(out + p.H, c, acc_post[i]);
     }
 }
 
-// out[which][col] = sum over blocks of part[block][which][col], in block order within each of
-// eight slices, then over the slices.
-__global__ void __launch_bounds__(256) norm_columns_kernel(const float* part, int blocks, int H, float* dpre,
-                                                           float* dpost, float* dgate) {
-    __shared__ float sums[8][32];
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    float* out = blockIdx.y == 0 ? dpre : (blockIdx.y == 1 ? dpost : dgate);
-    if (!out) return;
-    const int col = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    if (col < H) {
-        const float* src = part + size_t(blockIdx.y) * H + col;
-        for (int b = slice; b < blocks; b += 8) s += src[size_t(b) * 3 * H];
+// dpre_w[col] = sum over blocks of part[block][0][col]; A[col] likewise from part[block][1] gives
+// dpost_w and a channel gate's gradient. 32 slices of the blocks, each in block order, then the
+// slices in order; a thread has four columns.
+__global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, int blocks, float* dpre, float* dpost,
+                                                           float* dgate) {
+    __shared__ float4 sums[32][8];
+    const int which = blockIdx.y, q = threadIdx.x & 7, slice = threadIdx.x >> 3;
+    if (which == 0 ? !dpre : !(dpost || dgate)) return;
+    const int col = blockIdx.x * 32 + 4 * q;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (col < p.H) {
+        const float* src = p.part + size_t(which) * p.H + col;
+#pragma unroll 4
+        for (int b = slice; b < blocks; b += 32) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + size_t(b) * 2 * p.H));
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
     }
-    sums[slice][lane] = s;
+    sums[slice][q] = s;
     __syncthreads();
-    if (slice == 0 && col < H) {
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x >= 32 || c >= p.H) return;
+    float a = 0.0f;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
-        out[col] = s;
+    for (int i = 0; i < 32; ++i) a += reinterpret_cast<const float*>(&sums[i][threadIdx.x >> 2])[threadIdx.x & 3];
+    if (which == 0) {
+        dpre[c] = a;
+        return;
     }
+    float v = p.block_scale, dv = p.block_scale;  // block_scale act(gate) and block_scale act'(gate)
+    if (p.gate_kind == GATE_CHANNEL) {
+        const float g = load1(p.gate, p.gate_f32, c), w = p.post_w ? p.w_offset + load1(p.post_w, p.w_f32, c) : 1.0f;
+        const float act = p.sigmoid ? sigmoid(g) : g;
+        dv *= p.sigmoid ? act * (1.0f - act) : 1.0f;
+        v *= act;
+        if (dgate) dgate[c] = a * dv * w;
+    }
+    if (dpost) dpost[c] = p.gate_kind == GATE_TOKEN || p.gate_kind == GATE_ELEMENT ? a : a * v;
 }
 
 // ------------------------------------------------------------------------------ host side
 struct NormShape {
     int nc, tpr, rows;  // chunks a thread, threads a row, rows a block
 };
-NormShape norm_shape(int H) {
+// A thread has one chunk of a row while the rows' blocks are few (the shortest way through a row:
+// 1.9 against 2.3 us for one row of 2048), two where they are many (half the threads at a barrier,
+// twice the loads in flight of each: 25.9 against 32.9 us for 8192 rows of 2048) and where 512
+// threads would not do.
+NormShape norm_shape(int H, long long T, int sm_count) {
     NormShape s;
     const int chunks = H / 8;
-    s.nc = chunks > 512 ? 2 : 1;
+    s.nc = chunks > 512 || (chunks > 32 && T * ((chunks + 31) / 32) > 32ll * sm_count) ? 2 : 1;
     s.tpr = ((chunks + s.nc - 1) / s.nc + 31) / 32 * 32;
     s.rows = s.tpr >= NORM_THREADS ? 1 : NORM_THREADS / s.tpr;
     return s;
 }
 
-int backward_blocks(int T, int rows, int sm_count) {
-    const int need = (T + rows - 1) / rows;
-    const int most = 2 * sm_count;
-    return need < most ? need : most;
-}
-// An upper bound that needs no device: the workspace query works without one.
-constexpr int MAX_BACKWARD_BLOCKS = 2 * 160;
+// An upper bound on the blocks of the backward pass that needs no device: the workspace query
+// works without one.
+constexpr int MAX_SMS = 160, MAX_BLOCKS_SM = 2;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -462,23 +575,43 @@ NormParams base_params(const redmoe_norm* N, int T, const void* gate, const Norm
 
 using NormKernel = void (*)(NormParams);
 
-#define NORM_PICK(kernel, NC, B)                                                                                       \
-    (hd ? (yd ? (xd ? kernel<1, 1, 1, NC, B> : kernel<1, 1, 0, NC, B>) : (xd ? kernel<1, 0, 1, NC, B> : kernel<1, 0, 0, NC, B>)) \
-        : (yd ? (xd ? kernel<0, 1, 1, NC, B> : kernel<0, 1, 0, NC, B>) : (xd ? kernel<0, 0, 1, NC, B> : kernel<0, 0, 0, NC, B>)))
+// Every combination of types; without y its type does not matter.
+#define NORM_TYPES(kernel, ...)                                                                                        \
+    (hd ? (yd ? (xd ? kernel<1, 1, 1, __VA_ARGS__> : kernel<1, 1, 0, __VA_ARGS__>)                                     \
+              : (xd ? kernel<1, 0, 1, __VA_ARGS__> : kernel<1, 0, 0, __VA_ARGS__>))                                    \
+        : (yd ? (xd ? kernel<0, 1, 1, __VA_ARGS__> : kernel<0, 1, 0, __VA_ARGS__>)                                     \
+              : (xd ? kernel<0, 0, 1, __VA_ARGS__> : kernel<0, 0, 0, __VA_ARGS__>)))
+#define NORM_ROWS(kernel, B)                                                                                           \
+    (nc == 2 ? (threads <= 256 ? NORM_TYPES(kernel, 2, B, 256) : NORM_TYPES(kernel, 2, B, 512))                        \
+             : (threads <= 256 ? NORM_TYPES(kernel, 1, B, 256) : NORM_TYPES(kernel, 1, B, 512)))
 
 NormKernel pick_forward(const redmoe_norm* N, int nc, bool branch) {
-    const bool hd = N->h_dtype == DT_BF16, xd = N->x_dtype == DT_BF16;
-    const bool yd = branch && N->y_dtype == DT_BF16;  // without y its type does not matter
-    if (branch) return nc == 1 ? NORM_PICK(norm_forward_kernel, 1, true) : NORM_PICK(norm_forward_kernel, 2, true);
-    return nc == 1 ? NORM_PICK(norm_forward_kernel, 1, false) : NORM_PICK(norm_forward_kernel, 2, false);
+    const bool hd = N->h_dtype == DT_BF16, xd = N->x_dtype == DT_BF16, yd = branch && N->y_dtype == DT_BF16;
+    if (branch) return nc == 1 ? NORM_TYPES(norm_forward_kernel, 1, true) : NORM_TYPES(norm_forward_kernel, 2, true);
+    return nc == 1 ? NORM_TYPES(norm_forward_kernel, 1, false) : NORM_TYPES(norm_forward_kernel, 2, false);
 }
-NormKernel pick_backward(const redmoe_norm* N, int nc, bool branch) {
-    const bool hd = N->h_dtype == DT_BF16, xd = N->x_dtype == DT_BF16;
-    const bool yd = branch && N->y_dtype == DT_BF16;
-    if (branch) return nc == 1 ? NORM_PICK(norm_backward_kernel, 1, true) : NORM_PICK(norm_backward_kernel, 2, true);
-    return nc == 1 ? NORM_PICK(norm_backward_kernel, 1, false) : NORM_PICK(norm_backward_kernel, 2, false);
+NormKernel pick_backward(const redmoe_norm* N, int nc, int threads, bool branch) {
+    const bool hd = N->h_dtype == DT_BF16, xd = N->x_dtype == DT_BF16, yd = branch && N->y_dtype == DT_BF16;
+    return branch ? NORM_ROWS(norm_backward_kernel, true) : NORM_ROWS(norm_backward_kernel, false);
 }
-#undef NORM_PICK
+#undef NORM_ROWS
+#undef NORM_TYPES
+
+int units(int dt) { return dt == DT_F32 ? 2 : 1; }
+
+// Shared memory of a kernel that walks rows, and with it p.ahead: two rows in flight where `want`
+// blocks of an SM can hold them, else one, else none.
+int rows_smem(NormParams& p, const NormShape& s, int want, int max_smem) {
+    const int stage = s.nc * p.units * s.tpr * s.rows * 16, fixed = 2 * p.H * 4, own = 2 * 8 * RED * 4;
+    const int room = max_smem / want - own - (want > 1 ? 1024 : 0);  // 1 KiB of every block is the system's
+    p.ahead = 2;
+    while (p.ahead > 0 && fixed + (p.ahead + 1) * stage > room) --p.ahead;
+    const int smem = fixed + (p.ahead + 1) * stage, ends = (s.rows - 1) * 2 * p.H * 4;
+    return smem > ends ? smem : ends;
+}
+bool set_smem(NormKernel kern, int smem) {
+    return smem <= 40 * 1024 || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+}
 
 }  // namespace
 
@@ -519,24 +652,24 @@ redmoe_status redmoe_norm_forward(const redmoe_norm* N, const void* h, const voi
     const redmoe_status st = norm_forward_check(N, h, y, gate, T, h_out, x);
     if (st != REDMOE_OK || T == 0) return st;
     const bool branch = y != nullptr;
-    const NormShape s = norm_shape(N->hidden);
+    DevInfo di;
+    if (!get_dev_info(&di)) return REDMOE_ERR_CUDA;
+    const NormShape s = norm_shape(N->hidden, T, di.sm_count);
     NormParams p = base_params(N, T, gate, s);
     p.h = h;
     p.y = y;
     p.h_out = h_out;
     p.x = x;
-    const NormKernel kern = pick_forward(N, s.nc, branch);
-    const unsigned grid = unsigned((T + (long long)s.rows - 1) / s.rows);
-    kern<<<grid, s.tpr * s.rows, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const long long need = (T + (long long)s.rows - 1) / s.rows;
+    const int threads = s.tpr * s.rows;
+    pick_forward(N, s.nc, branch)<<<unsigned(need), threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 size_t redmoe_norm_workspace_bytes(const redmoe_norm* N, int32_t T) {
     if (T < 0 || check_norm(N) != REDMOE_OK) return 0;
-    const NormShape s = norm_shape(N->hidden);
-    const long long need = ((long long)T + s.rows - 1) / s.rows;
-    const long long blocks = need < MAX_BACKWARD_BLOCKS ? need : MAX_BACKWARD_BLOCKS;
-    return 256 + align256(size_t(blocks) * 3 * N->hidden * 4);
+    const long long blocks = T < MAX_SMS * MAX_BLOCKS_SM ? T : MAX_SMS * MAX_BLOCKS_SM;  // a row each, at most
+    return 256 + align256(size_t(blocks) * 2 * N->hidden * 4);
 }
 
 redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, const void* y, const void* gate,
@@ -595,7 +728,7 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     }
     DevInfo di;
     if (!get_dev_info(&di)) return REDMOE_ERR_CUDA;
-    const NormShape s = norm_shape(N->hidden);
+    const NormShape s = norm_shape(N->hidden, T, di.sm_count);
     NormParams p = base_params(N, T, gate, s);
     p.h = h_out;
     p.y = y;
@@ -608,15 +741,18 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     p.want_pre = dpre_w != nullptr;
     p.want_post = dpost_w != nullptr;
     p.want_gate = dgate != nullptr && channel;
-    const int sms = di.sm_count < MAX_BACKWARD_BLOCKS / 2 ? di.sm_count : MAX_BACKWARD_BLOCKS / 2;
-    const int blocks = backward_blocks(T, s.rows, sms);
-    // at most 21,504 bytes (H = 256: eight groups): below what a launch gets without asking
-    const size_t smem = work ? size_t(s.rows - 1) * 3 * p.H * 4 : 0;
-    const NormKernel kern = pick_backward(N, s.nc, branch);
-    kern<<<blocks, s.tpr * s.rows, smem, stm>>>(p);
+    const int threads = s.tpr * s.rows, want = threads <= 256 ? MAX_BLOCKS_SM : 1;
+    const long long all = (T + (long long)s.rows - 1) / s.rows, most = want * (di.sm_count < MAX_SMS ? di.sm_count : MAX_SMS);
+    const int blocks = int(all < most ? all : most);
+    p.units = 2 * units(N->h_dtype) + units(N->x_dtype) + (branch ? units(N->y_dtype) : 0) +
+              (branch && N->gate_kind == GATE_ELEMENT ? units(N->gate_dtype) : 0);
+    const int smem = rows_smem(p, s, want, di.max_smem_optin);
+    const NormKernel kern = pick_backward(N, s.nc, threads, branch);
+    if (!set_smem(kern, smem)) return REDMOE_ERR_CUDA;
+    kern<<<blocks, threads, smem, stm>>>(p);
     if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
     if (!work) return REDMOE_OK;
-    norm_columns_kernel<<<dim3((p.H + 31) / 32, 3), 256, 0, stm>>>(p.part, blocks, p.H, dpre_w, dpost_w,
+    norm_columns_kernel<<<dim3((p.H + 31) / 32, 2), 256, 0, stm>>>(p, blocks, dpre_w, dpost_w,
                                                                    p.want_gate ? static_cast<float*>(dgate) : nullptr);
     return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }

@@ -18,21 +18,76 @@ __device__ __forceinline__ uint4 ld_row(const void* p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
+
+// Eight fp32 values as pairs: one packed instruction works on two.
+struct F8 {
+    float2 v[4];
+};
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ F8 mul(const F8& a, const F8& b) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+    return r;
+}
+__device__ __forceinline__ F8 mul(const F8& a, float b) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], both(b));
+    return r;
+}
+__device__ __forceinline__ F8 fma(const F8& a, const F8& b, const F8& c) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+    return r;
+}
+__device__ __forceinline__ F8 fma(const F8& a, float b, const F8& c) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], both(b), c.v[i]);
+    return r;
+}
+__device__ __forceinline__ F8 add(const F8& a, float b) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = __fadd2_rn(a.v[i], both(b));
+    return r;
+}
+__device__ __forceinline__ void dot(const F8& a, const F8& b, float2& s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
+}
+__device__ __forceinline__ F8 fill8(float a) {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = both(a);
+    return r;
+}
+__device__ __forceinline__ F8 bf16x8(const uint4& a) {
+    F8 r;
+    r.v[0] = make_float2(bf16lo(a.x), bf16hi(a.x));
+    r.v[1] = make_float2(bf16lo(a.y), bf16hi(a.y));
+    r.v[2] = make_float2(bf16lo(a.z), bf16hi(a.z));
+    r.v[3] = make_float2(bf16lo(a.w), bf16hi(a.w));
+    return r;
+}
+__device__ __forceinline__ F8 f32x8(const uint4& a, const uint4& b) {
+    F8 r;
+    r.v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+    r.v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    r.v[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+    r.v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    return r;
+}
+
+// One chunk as it comes from memory.
 template <int DT> struct Raw8;
 template <> struct Raw8<DT_BF16> {
     uint4 a;
-    __device__ __forceinline__ void load(const void* p, size_t chunk) {
-        a = ld_row(static_cast<const uint4*>(p) + chunk);
-    }
+    __device__ __forceinline__ void load(const void* p, size_t chunk) { a = ld_row(static_cast<const uint4*>(p) + chunk); }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16lo(w[i]);
-            v[2 * i + 1] = bf16hi(w[i]);
-        }
-    }
+    __device__ __forceinline__ F8 get() const { return bf16x8(a); }
 };
 template <> struct Raw8<DT_F32> {
     uint4 a, b;
@@ -41,12 +96,22 @@ template <> struct Raw8<DT_F32> {
         b = ld_row(static_cast<const uint4*>(p) + 2 * chunk + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    }
+    __device__ __forceinline__ F8 get() const { return f32x8(a, b); }
 };
+
+// A chunk whose type is known at run time (weights and gates: cached loads).
+struct RawAny {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void* p, bool f32, size_t chunk) {
+        const uint4* q = static_cast<const uint4*>(p) + (f32 ? 2 * chunk : chunk);
+        a = __ldg(q);
+        if (f32) b = __ldg(q + 1);
+    }
+    __device__ __forceinline__ F8 get(bool f32) const { return f32 ? f32x8(a, b) : bf16x8(a); }
+};
+__device__ __forceinline__ float load1(const void* p, bool f32, size_t i) {
+    return f32 ? __ldg(static_cast<const float*>(p) + i) : bf16f(__ldg(static_cast<const uint16_t*>(p) + i));
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);  // round to nearest even, NaN stays NaN
@@ -54,36 +119,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 template <int DT>
-__device__ __forceinline__ void store8(void* p, size_t chunk, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* p, size_t chunk, const F8& f) {
     if (DT == DT_BF16) {
-        static_cast<uint4*>(p)[chunk] =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        static_cast<uint4*>(p)[chunk] = make_uint4(pack_bf16(f.v[0].x, f.v[0].y), pack_bf16(f.v[1].x, f.v[1].y),
+                                                   pack_bf16(f.v[2].x, f.v[2].y), pack_bf16(f.v[3].x, f.v[3].y));
     } else {
         float4* q = static_cast<float4*>(p) + 2 * chunk;
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        q[0] = make_float4(f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y);
+        q[1] = make_float4(f.v[2].x, f.v[2].y, f.v[3].x, f.v[3].y);
     }
-}
-
-// Vectors shared by all rows (weights, channel gates), type known at run time: cached loads.
-__device__ __forceinline__ void load8_shared(const void* p, bool f32, size_t chunk, float (&v)[8]) {
-    if (f32) {
-        const float4 a = __ldg(static_cast<const float4*>(p) + 2 * chunk);
-        const float4 b = __ldg(static_cast<const float4*>(p) + 2 * chunk + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = __ldg(static_cast<const uint4*>(p) + chunk);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16lo(w[i]);
-            v[2 * i + 1] = bf16hi(w[i]);
-        }
-    }
-}
-__device__ __forceinline__ float load1(const void* p, bool f32, size_t i) {
-    return f32 ? __ldg(static_cast<const float*>(p) + i) : bf16f(__ldg(static_cast<const uint16_t*>(p) + i));
 }
 
 }  // namespace

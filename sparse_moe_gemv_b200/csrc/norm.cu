@@ -106,10 +106,40 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int tpr, in
     }
 }
 
+// Six sums over the group at once: eight lanes' worth of values is halved three times while the warp
+// is (nine shuffles for six sums), lane 4 v ends with value v; behind the barrier a quad of lanes adds
+// one value's warps. buf: [6][16].
+constexpr int RED6 = 6 * 16;
+__device__ __forceinline__ void group_sum6(float (&v)[6], float* buf, int tpr, int group, int wig) {
+    const int l = threadIdx.x & 31;
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // lanes 16 .. 31 keep values 4 .. 7 (6 and 7 are none), the others 0 .. 3
+        const float hi = i < 2 ? v[4 + (i & 1)] : 0.0f;
+        a[i] = (l & 16 ? hi : v[i]) + __shfl_xor_sync(FULL, l & 16 ? v[i] : hi, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) b[i] = (l & 8 ? a[2 + i] : a[i]) + __shfl_xor_sync(FULL, l & 8 ? a[i] : a[2 + i], 8);
+    float c = (l & 4 ? b[1] : b[0]) + __shfl_xor_sync(FULL, l & 4 ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(FULL, c, 2);
+    c += __shfl_xor_sync(FULL, c, 1);
+    if (tpr > 32) {
+        if ((l & 3) == 0 && l < 24) buf[(l >> 2) * 16 + wig] = c;
+        asm volatile("bar.sync %0, %1;" :: "r"(group + 1), "r"(tpr) : "memory");
+        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (l < 24) f = *reinterpret_cast<const float4*>(buf + 4 * l);  // value l / 4, warps 4 (l % 4) ..
+        c = (f.x + f.y) + (f.z + f.w);
+        c += __shfl_xor_sync(FULL, c, 1);
+        c += __shfl_xor_sync(FULL, c, 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(FULL, c, 4 * i);
+}
+
 // The places of warps that a group does not have, read as zeros by group_sum (whose barrier
 // publishes them).
-__device__ __forceinline__ void clear_unused(float* a, float* b, int lane, int tpr) {
-    for (int i = lane; i < RED; i += tpr)
+__device__ __forceinline__ void clear_unused(float* a, float* b, int n, int lane, int tpr) {
+    for (int i = lane; i < n; i += tpr)
         if (i % 16 >= tpr / 32) a[i] = b[i] = 0.0f;
 }
 
@@ -136,7 +166,7 @@ __global__ void __launch_bounds__(512, 2) norm_forward_kernel(const NormParams p
     const long long t = (long long)blockIdx.x * rows + group;
     if (t >= p.T) return;  // whole groups only: the group barriers stay complete
     const size_t row = size_t(t) * p.chunks;
-    clear_unused(red[0][group], red[1][group], lane, p.tpr);
+    clear_unused(red[0][group], red[1][group], RED, lane, p.tpr);
 
     Raw8<HD> hr[NC];
     Raw8<YD> yr[NC];
@@ -270,19 +300,22 @@ __device__ __forceinline__ void shared_vectors(const NormParams& p, bool branch,
     }
 }
 
-// Backward. Without an element or token gate, the gradients of post_w and of a channel gate are
-// per-column multiples of one sum, A = sum_t G y r1: norm_columns_kernel makes both from it. With
-// them A takes each row's gate in and is dpost_w itself.
+// Backward. The sums that a row needs are six, all of what is read:
+//   S = {h^2, dx pre h, y^2, dh_out e, dx pre e, h e},  e = y post (times an element gate)
+// since sum G e = S3 + r2 (S4 - k2 S5) with k2 = r2^2 S1 / H: one reduction a row, where summing G e
+// itself would wait for a first one. Without an element or token gate, the gradients of post_w and of
+// a channel gate are per-column multiples of one sum, A = sum_t G y r1: norm_columns_kernel makes
+// both from it. With them A takes each row's gate in and is dpost_w itself.
 template <int HD, int YD, int XD, int NC, bool BRANCH, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward_kernel(const NormParams p) {
     constexpr int UH = HD == DT_F32 ? 2 : 1, UX = XD == DT_F32 ? 2 : 1, UY = BRANCH ? (YD == DT_F32 ? 2 : 1) : 0;
     constexpr int AT_G = UH, AT_X = 2 * UH, AT_Y = AT_X + UX, AT_GATE = AT_Y + UY;  // units: h_out, dh_out, dx, y, gate
     extern __shared__ __align__(16) float dyn[];  // post, pre [H] each, then the rows' units; at the end
                                                   // the column sums [groups - 1][2][H]
-    __shared__ __align__(16) float red[2][8][RED];
+    __shared__ __align__(16) float red[2][8][RED6];
     const int group = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr, wig = lane / 32;
     const int rows = blockDim.x / p.tpr;
-    clear_unused(red[0][group], red[1][group], lane, p.tpr);
+    clear_unused(red[0][group], red[1][group], RED6, lane, p.tpr);
     const int stride = blockDim.x * 16, chunk_bytes = p.units * stride, stage_bytes = NC * chunk_bytes;
     const uint32_t post = smem_u32(dyn), pre = post + 4 * p.H, mine = pre + 4 * p.H + 16 * threadIdx.x;
     const bool has_x = p.dx != nullptr, has_g = p.dh_out != nullptr, post_norm = BRANCH && p.post_norm,
@@ -318,101 +351,101 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
     for (int i = 0; i < NC; ++i) acc_pre[i] = acc_post[i] = fill8(0.0f);
     for (; t < p.T; t += step) {
         const size_t row = size_t(t) * p.chunks;
-        float token = 1.0f, dtoken = 1.0f;
+        float kappa = tokens || element ? p.block_scale : 1.0f, dtoken = 1.0f;
         if (tokens) {
-            token = load1(p.gate, p.gate_f32, t);
+            float token = load1(p.gate, p.gate_f32, t);
             if (p.sigmoid) {
                 token = sigmoid(token);
                 dtoken = token * (1.0f - token);
             }
+            kappa *= token;
         }
         ask(t + p.ahead * step);
         rows_wait(p.ahead);
         const uint32_t at = mine + use * stage_bytes;
         use = use == p.ahead ? 0 : use + 1;
 
-        // a thread's one chunk stays in registers between the sums; two would not fit beside the
+        // a thread's one chunk stays in registers across the sums; two would not fit beside the
         // column sums and are read again
-        F8 h, a, y;
+        F8 h, a, y, dho, v;
         auto read = [&](uint32_t u) {
             h = lds8<UH>(u, stride);
+            if (has_g) dho = lds8<UH>(u + AT_G * stride, stride);
+            else dho = fill8(0.0f);
             if (has_x) a = lds8<UX>(u + AT_X * stride, stride);
-            if constexpr (BRANCH) y = lds8<UY>(u + AT_Y * stride, stride);
-        };
-        float2 q0 = both(0.0f), q1 = q0, q2 = q0;  // h_out^2, dx pre h_out, y^2
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            if (c >= p.chunks) continue;
-            read(at + i * chunk_bytes);
-            if (has_x) {
-                dot(h, h, q0);
-                dot(mul(a, lds8f(pre + 32 * c)), h, q1);
+            if constexpr (BRANCH) {
+                y = lds8<UY>(u + AT_Y * stride, stride);
+                if (element) {
+                    v = p.gate_f32 ? lds8<2>(u + AT_GATE * stride, stride) : lds8<1>(u + AT_GATE * stride, stride);
+                    if (p.sigmoid) v = sigmoid(v);
+                }
             }
-            if (BRANCH) dot(y, y, q2);
+        };
+        float s[6];
+        {
+            float2 q[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) q[i] = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = lane + i * p.tpr;
+                if (c >= p.chunks) continue;
+                read(at + i * chunk_bytes);
+                F8 e;
+                if constexpr (BRANCH) {
+                    e = mul(y, lds8f(post + 32 * c));
+                    if (element) e = mul(e, v);
+                    dot(y, y, q[2]);
+                    dot(dho, e, q[3]);
+                }
+                if (has_x) {
+                    const F8 ap = mul(a, lds8f(pre + 32 * c));
+                    dot(h, h, q[0]);
+                    dot(ap, h, q[1]);
+                    if constexpr (BRANCH) {
+                        dot(ap, e, q[4]);
+                        dot(h, e, q[5]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 6; ++i) s[i] = q[i].x + q[i].y;
         }
-        float s[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
-        group_sum<3>(s, red[turn][group], p.tpr, group, wig);
+        group_sum6(s, red[turn][group], p.tpr, group, wig);
         turn ^= 1;
-        const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps));
-        const float k2 = r2 * r2 * (s[1] * p.inv_h);
+        const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps)), k2 = r2 * r2 * (s[1] * p.inv_h);
         const float r1 = post_norm ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.0f;
-        q0 = q1 = both(0.0f);  // c y, and the token gate's b u
-        F8 G[NC];
+        const float sum = has_x ? fmaf(r2, fmaf(-k2, s[5], s[4]), s[3]) : s[3];  // of G e
+        const float k1 = post_norm ? r1 * r1 * (sum * p.inv_h) : 0.0f, f1 = r1 * kappa;
+        if (tokens && p.dgate && lane == 0)
+            static_cast<float*>(p.dgate)[t] = p.block_scale * dtoken * r1 * sum;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
             if (c >= p.chunks) continue;
-            const uint32_t u = at + i * chunk_bytes;
-            if (NC > 1) read(u);
-            if (has_g) G[i] = lds8<UH>(u + AT_G * stride, stride);
-            else G[i] = fill8(0.0f);
+            if (NC > 1) read(at + i * chunk_bytes);
+            F8 G = dho;
             if (has_x) {
                 acc_pre[i] = fma(a, mul(h, r2), acc_pre[i]);
-                G[i] = fma(fma(h, -k2, mul(a, lds8f(pre + 32 * c))), r2, G[i]);
+                G = fma(fma(h, -k2, mul(a, lds8f(pre + 32 * c))), r2, G);
             }
             if constexpr (!BRANCH) {
-                store8<HD>(p.dh, row + c, G[i]);
+                store8<HD>(p.dh, row + c, G);
             } else {
-                store8<HD>(p.dh, row + c, mul(G[i], p.res_scale));
-                const F8 yn = mul(y, r1), w = lds8f(post + 32 * c);
+                store8<HD>(p.dh, row + c, mul(G, p.res_scale));
+                F8 w = lds8f(post + 32 * c);
                 if (element) {
-                    F8 v = p.gate_f32 ? lds8<2>(u + AT_GATE * stride, stride) : lds8<1>(u + AT_GATE * stride, stride);
-                    G[i] = mul(G[i], p.block_scale);
-                    F8 dg = mul(mul(G[i], yn), w);
-                    if (p.sigmoid) {
-                        v = sigmoid(v);
-                        dg = mul(dg, fma(mul(v, -1.0f), v, v));  // v (1 - v)
-                    }
                     if (p.dgate) {
+                        F8 dg = mul(mul(mul(G, y), f1), w);
+                        if (p.sigmoid) dg = mul(dg, fma(mul(v, -1.0f), v, v));  // v (1 - v)
                         if (p.gate_f32) store8<DT_F32>(p.dgate, row + c, dg);
                         else store8<DT_BF16>(p.dgate, row + c, dg);
                     }
-                    G[i] = mul(G[i], v);
-                } else if (tokens) {
-                    G[i] = mul(G[i], p.block_scale);
-                    dot(mul(G[i], yn), w, q1);
-                    G[i] = mul(G[i], token);
+                    G = mul(G, v);
                 }
-                acc_post[i] = fma(G[i], yn, acc_post[i]);
-                G[i] = mul(G[i], w);  // c, or dy where y is not normalised
-                if (post_norm) dot(G[i], y, q0);
-                else store8<YD>(p.dy, row + c, G[i]);
+                acc_post[i] = fma(G, mul(y, f1), acc_post[i]);
+                store8<YD>(p.dy, row + c, mul(fma(y, -k1, mul(G, w)), f1));
             }
-        }
-        if (!post_norm && !tokens) continue;
-        float u[2] = {q0.x + q0.y, q1.x + q1.y};
-        group_sum<2>(u, red[turn][group], p.tpr, group, wig);
-        turn ^= 1;
-        if (tokens && p.dgate && lane == 0) static_cast<float*>(p.dgate)[t] = u[1] * dtoken;
-        if (!post_norm) continue;
-        const float k1 = r1 * r1 * (u[0] * p.inv_h);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            if (c >= p.chunks) continue;
-            if constexpr (BRANCH && NC > 1) y = lds8<UY>(at + i * chunk_bytes + AT_Y * stride, stride);
-            store8<YD>(p.dy, row + c, mul(fma(y, -k1, G[i]), r1));
         }
     }
     if (!p.part) return;
@@ -602,7 +635,7 @@ int units(int dt) { return dt == DT_F32 ? 2 : 1; }
 // Shared memory of a kernel that walks rows, and with it p.ahead: two rows in flight where `want`
 // blocks of an SM can hold them, else one, else none.
 int rows_smem(NormParams& p, const NormShape& s, int want, int max_smem) {
-    const int stage = s.nc * p.units * s.tpr * s.rows * 16, fixed = 2 * p.H * 4, own = 2 * 8 * RED * 4;
+    const int stage = s.nc * p.units * s.tpr * s.rows * 16, fixed = 2 * p.H * 4, own = 2 * 8 * RED6 * 4;
     const int room = max_smem / want - own - (want > 1 ? 1024 : 0);  // 1 KiB of every block is the system's
     p.ahead = 2;
     while (p.ahead > 0 && fixed + (p.ahead + 1) * stage > room) --p.ahead;

@@ -14,9 +14,10 @@
 // brackets is the same (p sums to 1) and even counts leave no rounding behind.
 //
 // Both directions are bound by memory: the logits are read once (forward) or read and written
-// once (backward), rows that do not count are not read. One warp takes a row, a lane the same
-// columns of every row, so the column sums of P stay in registers until the warp's rows are done;
-// the next row is asked for while one is worked on, its mask byte a row earlier. Forward, the
+// once (backward), rows that do not count are not read. A warp takes a row, or eight lanes of it where
+// a row is short (up to 128 columns), a lane the same columns of every row, so the column sums of P
+// stay in registers until the warp's rows are done; the next row is asked for while one is worked on,
+// its mask byte a row earlier. Forward, the
 // blocks of a cluster add their sums through distributed shared memory, and the last block to
 // finish adds the clusters': a single launch. Sums over rows are made in a fixed order (lane,
 // warp, block, cluster), counts are integers: results do not depend on timing.
@@ -31,21 +32,22 @@ constexpr int BAL_CLUSTER = 4;
 constexpr int BAL_MAX_CLUSTERS = 80;  // two blocks an SM, 160 SMs
 __host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }  // a row of sums in the workspace
 
-// How a lane's values map to columns: VEC consecutive values per chunk, chunk lane + 32 i.
-// VEC > 1 needs E % VEC == 0 (whole 16-byte chunks in every row), VEC == 1 takes any E.
-template <int DT, int VEC, int NCH>
+// How a row lies over its LPR lanes: VEC consecutive values per chunk, chunk l + LPR i for lane l.
+// VEC > 1 needs E % VEC == 0 (whole 16-byte chunks in every row), VEC == 1 takes any E. Columns
+// beyond E, and rows that are not read, are -infinity.
+template <int DT, int VEC, int NCH, int LPR>
 struct RowOf {
     static constexpr int N = NCH * VEC, W = VEC == 1 ? 1 : 4;  // values, words a chunk
     uint32_t w[NCH][W];
 
-    __device__ __forceinline__ void load(const void* logits, size_t row, int E, int lane) {
-        constexpr uint32_t NONE = DT == DT_F32 ? 0xff800000u : 0xff80ff80u;  // -infinity
+    __device__ __forceinline__ void load(const void* logits, size_t row, int E, int l, bool live) {
+        constexpr uint32_t NONE = DT == DT_F32 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = lane + 32 * i;
+            const int c = l + LPR * i;
 #pragma unroll
             for (int j = 0; j < W; ++j) w[i][j] = NONE;
-            if (c * VEC >= E) continue;
+            if (!live || c * VEC >= E) continue;
             if constexpr (VEC == 1) {
                 if (DT == DT_F32) w[i][0] = static_cast<const uint32_t*>(logits)[row + c];
                 else w[i][0] = static_cast<const uint16_t*>(logits)[row + c] * 0x10001u;
@@ -55,73 +57,79 @@ struct RowOf {
             }
         }
     }
-    __device__ __forceinline__ void get(float (&v)[N]) const {
+    __device__ __forceinline__ float value(int k) const {
+        const uint32_t u = w[k / VEC][VEC == 1 ? 0 : DT == DT_F32 ? k % VEC : k % VEC / 2];
+        if (DT == DT_F32) return __uint_as_float(u);
+        return k & 1 ? bf16hi(u) : bf16lo(u);
+    }
+    __device__ __forceinline__ void get(float2 (&v)[N / 2]) const {
 #pragma unroll
-        for (int i = 0; i < NCH; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if (DT == DT_F32) v[i * VEC + j] = __uint_as_float(w[i][j % W]);
-                else v[i * VEC + j] = j & 1 ? bf16hi(w[i][j / 2]) : bf16lo(w[i][j / 2]);
-            }
+        for (int k = 0; k < N; k += 2) v[k / 2] = make_float2(value(k), value(k + 1));
     }
 };
 
-__device__ __forceinline__ float warp_max(float v) {
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     return v;
 }
+__device__ __forceinline__ float2 all2(float a) { return make_float2(a, a); }
 
-// v[] becomes exp(v - max) and z their sum over the row; returns the maximum, or false in `any`
-// where the row allows no expert. fmaxf drops a NaN, the sum does not: a row that holds one comes
-// out NaN whole. The fast exponential is off by about 2 + 1.2 |v - max| units, which is least where
-// the probability is large.
-template <int N>
-__device__ __forceinline__ float row_exp(float (&v)[N], float& z, bool& any) {
-    const float none = __uint_as_float(0xff800000u);
-    float m = v[0];
+// v[] becomes exp(v - max) and z their sum over the row; returns the maximum. A row that holds a NaN
+// comes out NaN whole; one of -infinity throughout (`any` false) comes out zero, with z = 0. The fast
+// exponential is off by about 2 + 1.2 |v - max| units, which is least where the probability is large.
+template <int N2, int LPR>
+__device__ __forceinline__ float row_exp(float2 (&v)[N2], float& z, bool& any) {
+    float m = max_nan(v[0].x, v[0].y);
 #pragma unroll
-    for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-    m = warp_max(m);
-    any = true;
-    if (m == none) {  // -infinity throughout, unless a NaN hides behind fmaxf
-        bool other = false;
+    for (int i = 1; i < N2; ++i) m = max_nan(m, max_nan(v[i].x, v[i].y));
+    if constexpr (LPR == 32) {
+        asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
+    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) other = other || v[i] != none;
-        any = __any_sync(FULL, other);
+        for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(FULL, m, o));
     }
-    float s = 0.0f;
+    any = m != __uint_as_float(0xff800000u);
+    if (!any) m = 0.0f;
+    float2 s = all2(0.0f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = __expf(v[i] - m);
-        s += v[i];
+    for (int i = 0; i < N2; ++i) {
+        const float2 d = __fadd2_rn(v[i], all2(-m));
+        v[i] = make_float2(__expf(d.x), __expf(d.y));
+        s = __fadd2_rn(s, v[i]);
     }
-    z = warp_sum(s);
+    z = row_sum<LPR>(s.x + s.y);
     return m;
 }
 
-// Rows of one warp, two ahead: the mask byte of the row after the next, the next row's data.
-template <int DT, int VEC, int NCH>
+// The rows of a lane's group, two ahead: the mask byte of the row after the next, the next row's data.
+template <int DT, int VEC, int NCH, int LPR>
 struct Walk {
-    RowOf<DT, VEC, NCH> next;
+    RowOf<DT, VEC, NCH, LPR> next;
     bool live, live2;  // of the next row and of the one behind it
     __device__ __forceinline__ static bool counts(const uint8_t* mask, long long t, int T) {
         return t < T && (!mask || __ldg(mask + t));
     }
     __device__ __forceinline__ void start(const void* logits, const uint8_t* mask, long long t, long long step, int T, int E,
-                                          int lane) {
+                                          int l) {
         live = counts(mask, t, T);
         live2 = counts(mask, t + step, T);
-        if (live) next.load(logits, size_t(t) * E, E, lane);
+        next.load(logits, size_t(t) * E, E, l, live);
     }
-    // Row t's values into v (if it is to be read at all), and on.
+    // Row t's values into v, and on; whether any of the warp's rows is to be looked at.
     __device__ __forceinline__ bool take(const void* logits, const uint8_t* mask, long long t, long long step, int T, int E,
-                                         int lane, float (&v)[NCH * VEC]) {
-        const bool now = live;
-        if (now) next.get(v);
+                                         int l, float2 (&v)[NCH * VEC / 2]) {
+        const bool now = __any_sync(FULL, live);
+        next.get(v);
         live = live2;
         live2 = counts(mask, t + 2 * step, T);
-        if (live) next.load(logits, size_t(t + step) * E, E, lane);
+        next.load(logits, size_t(t + step) * E, E, l, live);
         return now;
     }
 };
@@ -181,9 +189,9 @@ __device__ __forceinline__ uint32_t peer_u32(uint32_t a) {
     return v;
 }
 
-template <int DT, int VEC, int NCH, int WARPS>
+template <int DT, int VEC, int NCH, int LPR, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_forward_kernel(const BalanceParams p) {
-    constexpr int N = NCH * VEC, THREADS = 32 * WARPS;
+    constexpr int N2 = NCH * VEC / 2, THREADS = 32 * WARPS, RPW = 32 / LPR;  // pairs of a lane, rows of a warp
     extern __shared__ __align__(16) float sm[];
     float* cols = sm;                                         // [WARPS][E]; then [E]: the block's
     int* hist = reinterpret_cast<int*>(cols + WARPS * p.E);   // [E]
@@ -191,44 +199,64 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
     __shared__ int nsum[WARPS];
     __shared__ Tail tail;
     __shared__ bool last;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long step = (long long)gridDim.x * WARPS;
-    long long t = (long long)blockIdx.x * WARPS + warp;
-    Walk<DT, VEC, NCH> walk;
-    walk.start(p.logits, p.mask, t, step, p.T, p.E, lane);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
+    const long long step = (long long)gridDim.x * WARPS * RPW;
+    long long t0 = ((long long)blockIdx.x * WARPS + warp) * RPW;  // the warp's first row, then this lane's
+    long long t = t0 + lane / LPR;
+    Walk<DT, VEC, NCH, LPR> walk;
+    walk.start(p.logits, p.mask, t, step, p.T, p.E, l);
     for (int e = threadIdx.x; e < p.E; e += THREADS) hist[e] = 0;
     __syncthreads();
 
-    float acc[N] = {};
-    double z2 = 0.0;
+    float2 acc[N2];
+#pragma unroll
+    for (int i = 0; i < N2; ++i) acc[i] = all2(0.0f);
+    float z2 = 0.0f;
     int rows = 0;
-    for (; t < p.T; t += step) {
-        const bool live = walk.live;
+    for (; t0 < p.T; t0 += step, t += step) {
         int id = -1;
-        if (live && lane < p.k) id = p.ids[size_t(t) * p.k + lane];
-        float v[N];
-        if (!walk.take(p.logits, p.mask, t, step, p.T, p.E, lane, v)) continue;
+        if (walk.live && l < p.k) id = __ldg(p.ids + size_t(t) * p.k + l);
+        float2 v[N2];
+        if (!walk.take(p.logits, p.mask, t, step, p.T, p.E, l, v)) continue;
         float z;
         bool any;
-        const float m = row_exp<N>(v, z, any);
-        if (!any) continue;
-        const float inv = 1.0f / z;
+        const float m = row_exp<N2, LPR>(v, z, any);
+        const float inv = any ? __fdividef(1.0f, z) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
-        const float lse = m + logf(z);
-        z2 += double(lse) * double(lse);
-        ++rows;
-        if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
-    }
-#pragma unroll
-    for (int i = 0; i < NCH; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int e = (lane + 32 * i) * VEC + j;
-            if (e < p.E) cols[warp * p.E + e] = acc[i * VEC + j];
+        for (int i = 0; i < N2; ++i) acc[i] = __ffma2_rn(v[i], all2(inv), acc[i]);
+        if (any) {
+            const float lse = m + __logf(z);
+            z2 = fmaf(lse, lse, z2);
+            ++rows;
+            if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+            for (int j = l + LPR; j < p.k; j += LPR) {
+                id = __ldg(p.ids + size_t(t) * p.k + j);
+                if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+            }
         }
+    }
+    // the warp's groups: columns, squares and rows (equal in all lanes of a group)
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+            acc[i].x += __shfl_xor_sync(FULL, acc[i].x, o);
+            acc[i].y += __shfl_xor_sync(FULL, acc[i].y, o);
+        }
+        z2 += __shfl_xor_sync(FULL, z2, o);
+        rows += __shfl_xor_sync(FULL, rows, o);
+    }
+    if (lane < LPR) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int e = (l + LPR * i) * VEC + j, k = i * VEC + j;
+                if (e < p.E) cols[warp * p.E + e] = k & 1 ? acc[k / 2].y : acc[k / 2].x;
+            }
+    }
     if (lane == 0) {
-        zsum[warp] = z2;
+        zsum[warp] = double(z2);
         nsum[warp] = rows;
     }
     __syncthreads();
@@ -345,67 +373,67 @@ struct BalanceGradParams {
     void* dlogits;
 };
 
-template <int DT, int VEC, int NCH>
-__device__ __forceinline__ void store_logits(void* out, size_t row, int E, int lane, const float (&v)[NCH * VEC]) {
+template <int DT, int VEC, int NCH, int LPR>
+__device__ __forceinline__ void store_logits(void* out, size_t row, int E, int l, const float2 (&v)[NCH * VEC / 2]) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        const int c = lane + 32 * i;
+        const int c = l + LPR * i;
         if (c * VEC >= E) continue;
         if constexpr (VEC == 8) {
-            uint32_t q[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = pack_bf16(v[i * VEC + 2 * j], v[i * VEC + 2 * j + 1]);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row + size_t(c) * 8) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row + size_t(c) * 8) =
+                make_uint4(pack_bf16(v[4 * i].x, v[4 * i].y), pack_bf16(v[4 * i + 1].x, v[4 * i + 1].y),
+                           pack_bf16(v[4 * i + 2].x, v[4 * i + 2].y), pack_bf16(v[4 * i + 3].x, v[4 * i + 3].y));
         } else if constexpr (VEC == 4) {
             *reinterpret_cast<float4*>(static_cast<float*>(out) + row + size_t(c) * 4) =
-                make_float4(v[i * VEC], v[i * VEC + 1], v[i * VEC + 2], v[i * VEC + 3]);
-        } else if (DT == DT_F32) {
-            static_cast<float*>(out)[row + c] = v[i];
+                make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
         } else {
-            static_cast<uint16_t*>(out)[row + c] = uint16_t(pack_bf16(v[i], 0.0f));
+            const float x = i & 1 ? v[i / 2].y : v[i / 2].x;
+            if (DT == DT_F32) static_cast<float*>(out)[row + c] = x;
+            else static_cast<uint16_t*>(out)[row + c] = uint16_t(pack_bf16(x, 0.0f));
         }
     }
 }
 
-template <int DT, int VEC, int NCH, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) balance_backward_kernel(const BalanceGradParams p) {
-    constexpr int N = NCH * VEC;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long step = (long long)gridDim.x * WARPS;
-    long long t = (long long)blockIdx.x * WARPS + warp;
-    Walk<DT, VEC, NCH> walk;
-    walk.start(p.logits, p.mask, t, step, p.T, p.E, lane);
+template <int DT, int VEC, int NCH, int LPR, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_backward_kernel(const BalanceGradParams p) {
+    constexpr int N2 = NCH * VEC / 2, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
+    const long long step = (long long)gridDim.x * WARPS * RPW;
+    long long t0 = ((long long)blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;
+    Walk<DT, VEC, NCH, LPR> walk;
+    walk.start(p.logits, p.mask, t, step, p.T, p.E, l);
     const int n = max(*p.n_rows, 1);
     const int mean = int((long long)n * p.k / p.E);
     const float gb = p.grad[0] * (float(p.E) / (float(n) * float(p.k))) / float(n);
     const float gz = 2.0f * p.grad[1] / float(n);
-    float f[N];
+    float2 f[N2];  // the centred counts
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
+    for (int k = 0; k < 2 * N2; ++k) {
+        const int e = (l + LPR * (k / VEC)) * VEC + k % VEC;
+        const float c = e < p.E ? float(__ldg(p.counts + e) - mean) : 0.0f;
+        if (k & 1) f[k / 2].y = c;
+        else f[k / 2].x = c;
+    }
+    for (; t0 < p.T; t0 += step, t += step) {
+        float2 v[N2];
+        if (walk.take(p.logits, p.mask, t, step, p.T, p.E, l, v)) {
+            float z;
+            bool any;
+            const float m = row_exp<N2, LPR>(v, z, any);
+            float2 q = all2(0.0f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int e = (lane + 32 * i) * VEC + j;
-            f[i * VEC + j] = e < p.E ? float(__ldg(p.counts + e) - mean) : 0.0f;
-        }
-    for (; t < p.T; t += step) {
-        float v[N];
-        bool any = walk.take(p.logits, p.mask, t, step, p.T, p.E, lane, v);
-        float z, m;
-        if (any) m = row_exp<N>(v, z, any);
-        if (!any) {
+            for (int i = 0; i < N2; ++i) q = __ffma2_rn(v[i], f[i], q);
+            // p (gb (f - s) + gz lse); nothing in rows that do not count, whose v is zero
+            const float inv = any ? __fdividef(1.0f, z) : 0.0f, s = row_sum<LPR>(q.x + q.y) * inv;
+            const float zt = any ? gz * (m + __logf(z)) * inv : 0.0f, a = gb * inv;
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.0f;
+            for (int i = 0; i < N2; ++i)
+                v[i] = __fmul2_rn(v[i], __ffma2_rn(__fadd2_rn(f[i], all2(-s)), all2(a), all2(zt)));
         } else {
-            const float inv = 1.0f / z;
-            float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) s = fmaf(v[i], f[i], s);
-            s = warp_sum(s) * inv;
-            const float zt = gz * (m + logf(z)) * inv, a = gb * inv;
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] *= fmaf(a, f[i] - s, zt);
+            for (int i = 0; i < N2; ++i) v[i] = all2(0.0f);
         }
-        store_logits<DT, VEC, NCH>(p.dlogits, size_t(t) * p.E, p.E, lane, v);
+        if (t < p.T) store_logits<DT, VEC, NCH, LPR>(p.dlogits, size_t(t) * p.E, p.E, l, v);
     }
 }
 
@@ -424,30 +452,37 @@ redmoe_status check_balance(int dtype, int T, int E, int k) {
     return dtype == DT_F32 || dtype == DT_BF16 ? REDMOE_OK : REDMOE_ERR_UNSUPPORTED;
 }
 
-// Blocks that `warps` rows each keep busy, at most `most`.
-int balance_blocks(int T, int warps, int most) {
-    const int need = int((T + (long long)warps - 1) / warps);
+// Blocks of so many rows each that T rows need, at least one and at most `most`.
+int balance_blocks(int T, int rows, int most) {
+    const int need = int((T + (long long)rows - 1) / rows);
     return need < 1 ? 1 : (need < most ? need : most);
 }
 
-// 16-byte chunks where every row starts on one, else single values; the smallest number of
-// chunks a lane needs. W: warps of a block with up to 16 values a lane, and with more.
-#define BALANCE_PICK(kernel, W, W32)                                                                          \
-    do {                                                                                                      \
-        if (dtype == DT_BF16 && E % 8 == 0)                                                                   \
-            return E <= 256 ? kernel<DT_BF16, 8, 1, W> : (E <= 512 ? kernel<DT_BF16, 8, 2, W> : kernel<DT_BF16, 8, 4, W32>); \
-        if (dtype == DT_F32 && E % 4 == 0)                                                                    \
-            return E <= 128 ? kernel<DT_F32, 4, 1, W> : (E <= 512 ? kernel<DT_F32, 4, 4, W> : kernel<DT_F32, 4, 8, W32>); \
-        if (dtype == DT_F32)                                                                                  \
-            return E <= 128 ? kernel<DT_F32, 1, 4, W> : (E <= 512 ? kernel<DT_F32, 1, 16, W> : kernel<DT_F32, 1, 32, W32>); \
-        return E <= 128 ? kernel<DT_BF16, 1, 4, W> : (E <= 512 ? kernel<DT_BF16, 1, 16, W> : kernel<DT_BF16, 1, 32, W32>); \
+// 16-byte chunks where every row starts on one, else single values; eight lanes a row up to 128
+// columns; the smallest number of chunks a lane needs.
+constexpr int BAL_WARPS = 16;
+int rows_a_block(int E) { return E <= 128 ? 4 * BAL_WARPS : BAL_WARPS; }
+
+#define BALANCE_PICK(kernel)                                                                              \
+    do {                                                                                                  \
+        constexpr int F = DT_F32, B = DT_BF16, W = BAL_WARPS;                                             \
+        if (dtype == B && E % 8 == 0)                                                                     \
+            return E <= 64 ? kernel<B, 8, 1, 8, W> : E <= 128 ? kernel<B, 8, 2, 8, W> : E <= 256 ? kernel<B, 8, 1, 32, W> \
+                 : E <= 512 ? kernel<B, 8, 2, 32, W> : kernel<B, 8, 4, 32, W>;                            \
+        if (dtype == F && E % 4 == 0)                                                                     \
+            return E <= 32 ? kernel<F, 4, 1, 8, W> : E <= 128 ? kernel<F, 4, 4, 8, W> : E <= 256 ? kernel<F, 4, 2, 32, W> \
+                 : E <= 512 ? kernel<F, 4, 4, 32, W> : kernel<F, 4, 8, 32, W>;                            \
+        if (dtype == F)                                                                                   \
+            return E <= 32 ? kernel<F, 1, 4, 8, W> : E <= 128 ? kernel<F, 1, 16, 8, W> : E <= 512 ? kernel<F, 1, 16, 32, W> \
+                 : kernel<F, 1, 32, 32, W>;                                                               \
+        return E <= 32 ? kernel<B, 1, 4, 8, W> : E <= 128 ? kernel<B, 1, 16, 8, W> : E <= 512 ? kernel<B, 1, 16, 32, W> \
+             : kernel<B, 1, 32, 32, W>;                                                                   \
     } while (0)
 
 using ForwardKernel = void (*)(BalanceParams);
 using BackwardKernel = void (*)(BalanceGradParams);
-constexpr int FORWARD_WARPS = 16, BACKWARD_WARPS = 16, WIDE_WARPS = 16;  // wide: over 512 columns
-ForwardKernel pick_forward(int dtype, int E) { BALANCE_PICK(balance_forward_kernel, FORWARD_WARPS, WIDE_WARPS); }
-BackwardKernel pick_backward(int dtype, int E) { BALANCE_PICK(balance_backward_kernel, BACKWARD_WARPS, WIDE_WARPS); }
+ForwardKernel pick_forward(int dtype, int E) { BALANCE_PICK(balance_forward_kernel); }
+BackwardKernel pick_backward(int dtype, int E) { BALANCE_PICK(balance_backward_kernel); }
 #undef BALANCE_PICK
 
 }  // namespace
@@ -502,8 +537,7 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     p.ws_counts = reinterpret_cast<int32_t*>(base + w.counts);
     p.ws_tail = reinterpret_cast<Tail*>(base + w.tail);
     const ForwardKernel kern = pick_forward(logits_dtype, E);
-    const int warps = E <= 512 ? FORWARD_WARPS : WIDE_WARPS;
-    const int sums = 4 * (warps + 1) * E, ends = 32 * 32 * warps;  // columns and counts; the last block's
+    const int sums = 4 * (BAL_WARPS + 1) * E, ends = 32 * 32 * BAL_WARPS;  // columns and counts; the last block's
     const int smem = sums > ends ? sums : ends;                    // E = 1024: 69,632 bytes
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -511,10 +545,10 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     // whole clusters lie in one GPC each: about 24 of 25 places can be had
     const int places = di.sm_count * (E <= 512 ? 2 : 1) / BAL_CLUSTER * 24 / 25;
     const int most = places < 1 ? 1 : (places < BAL_MAX_CLUSTERS ? places : BAL_MAX_CLUSTERS);
-    const int clusters = balance_blocks(T, warps * BAL_CLUSTER, most);
+    const int clusters = balance_blocks(T, rows_a_block(E) * BAL_CLUSTER, most);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * BAL_CLUSTER);
-    cfg.blockDim = dim3(32 * warps);
+    cfg.blockDim = dim3(32 * BAL_WARPS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -549,8 +583,7 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     p.n_rows = n_rows;
     p.grad = grad_loss;
     p.dlogits = dlogits;
-    const int warps = E <= 512 ? BACKWARD_WARPS : WIDE_WARPS;
-    pick_backward(logits_dtype, E)<<<balance_blocks(T, warps, 2 * di.sm_count), 32 * warps, 0,
+    pick_backward(logits_dtype, E)<<<balance_blocks(T, rows_a_block(E), 2 * di.sm_count), 32 * BAL_WARPS, 0,
                                      static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }

@@ -16,8 +16,9 @@
 // Both directions are bound by memory: the logits are read once (forward) or read and written
 // once (backward), rows that do not count are not read. A warp takes a row, or eight lanes of it where
 // a row is short (up to 128 columns), a lane the same columns of every row, so the column sums of P
-// stay in registers until the warp's rows are done; the next row is asked for while one is worked on,
-// its mask byte a row earlier. Forward, the
+// stay in registers until the warp's rows are done. Rows are copied ahead into a ring of the warp's
+// in shared memory as the flat byte range that they are, whole 16-byte pieces whatever E is (short
+// and 16-bit rows need several in flight for full bandwidth). Forward, the
 // blocks of a cluster add their sums through distributed shared memory, and the last block to
 // finish adds the clusters': a single launch. Sums over rows are made in a fixed order (lane,
 // warp, block, cluster), counts are integers: results do not depend on timing.
@@ -28,45 +29,13 @@
 namespace redmoe {
 namespace {
 
+constexpr int BAL_WARPS = 16;
 constexpr int BAL_CLUSTER = 4;
 constexpr int BAL_MAX_CLUSTERS = 80;  // two blocks an SM, 160 SMs
 __host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }  // a row of sums in the workspace
 
-// How a row lies over its LPR lanes: VEC consecutive values per chunk, chunk l + LPR i for lane l.
-// VEC > 1 needs E % VEC == 0 (whole 16-byte chunks in every row), VEC == 1 takes any E. Columns
-// beyond E, and rows that are not read, are -infinity.
-template <int DT, int VEC, int NCH, int LPR>
-struct RowOf {
-    static constexpr int N = NCH * VEC, W = VEC == 1 ? 1 : 4;  // values, words a chunk
-    uint32_t w[NCH][W];
-
-    __device__ __forceinline__ void load(const void* logits, size_t row, int E, int l, bool live) {
-        constexpr uint32_t NONE = DT == DT_F32 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int c = l + LPR * i;
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[i][j] = NONE;
-            if (!live || c * VEC >= E) continue;
-            if constexpr (VEC == 1) {
-                if (DT == DT_F32) w[i][0] = static_cast<const uint32_t*>(logits)[row + c];
-                else w[i][0] = static_cast<const uint16_t*>(logits)[row + c] * 0x10001u;
-            } else {
-                const uint4 v = ld_row(static_cast<const char*>(logits) + (row * (DT == DT_F32 ? 4 : 2)) + size_t(c) * 16);
-                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-            }
-        }
-    }
-    __device__ __forceinline__ float value(int k) const {
-        const uint32_t u = w[k / VEC][VEC == 1 ? 0 : DT == DT_F32 ? k % VEC : k % VEC / 2];
-        if (DT == DT_F32) return __uint_as_float(u);
-        return k & 1 ? bf16hi(u) : bf16lo(u);
-    }
-    __device__ __forceinline__ void get(float2 (&v)[N / 2]) const {
-#pragma unroll
-        for (int k = 0; k < N; k += 2) v[k / 2] = make_float2(value(k), value(k + 1));
-    }
-};
+// A row lies over its LPR lanes in chunks of VEC consecutive values, chunk l + LPR i for lane l. VEC > 1
+// needs E % VEC == 0 (whole 16-byte chunks in every row), VEC == 1 takes any E.
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
     float r;
@@ -82,8 +51,8 @@ __device__ __forceinline__ float row_sum(float v) {
 __device__ __forceinline__ float2 all2(float a) { return make_float2(a, a); }
 
 // v[] becomes exp(v - max) and z their sum over the row; returns the maximum. A row that holds a NaN
-// comes out NaN whole; one of -infinity throughout (`any` false) comes out zero, with z = 0. The fast
-// exponential is off by about 2 + 1.2 |v - max| units, which is least where the probability is large.
+// comes out NaN whole; one of -infinity throughout (`any` false) comes out zero, with z = 0. Rounding
+// the exponent makes exp(v - max) off by about |v - max| units, least where the probability is large.
 template <int N2, int LPR>
 __device__ __forceinline__ float row_exp(float2 (&v)[N2], float& z, bool& any) {
     float m = max_nan(v[0].x, v[0].y);
@@ -100,37 +69,132 @@ __device__ __forceinline__ float row_exp(float2 (&v)[N2], float& z, bool& any) {
     float2 s = all2(0.0f);
 #pragma unroll
     for (int i = 0; i < N2; ++i) {
-        const float2 d = __fadd2_rn(v[i], all2(-m));
-        v[i] = make_float2(__expf(d.x), __expf(d.y));
+        const float2 d = __fmul2_rn(__fadd2_rn(v[i], all2(-m)), all2(LOG2E));
+        v[i] = make_float2(ex2(d.x), ex2(d.y));
         s = __fadd2_rn(s, v[i]);
     }
     z = row_sum<LPR>(s.x + s.y);
     return m;
 }
 
-// The rows of a lane's group, two ahead: the mask byte of the row after the next, the next row's data.
+// A warp's ring of row groups (RPW rows each) in shared memory. Rows of whole 16-byte chunks: each
+// lane copies, and later reads, its own chunks of its own row. Others: the group's flat byte range
+// with the pieces of 16 that it shares with its neighbours.
+__host__ __device__ constexpr int flat_bytes(int rows, int E, int size) { return (rows * E * size + 30) / 16 * 16 + 16; }
+
 template <int DT, int VEC, int NCH, int LPR>
-struct Walk {
-    RowOf<DT, VEC, NCH, LPR> next;
-    bool live, live2;  // of the next row and of the one behind it
-    __device__ __forceinline__ static bool counts(const uint8_t* mask, long long t, int T) {
-        return t < T && (!mask || __ldg(mask + t));
+struct Ring {
+    static constexpr int SIZE = DT == DT_F32 ? 4 : 2, RPW = 32 / LPR;
+    static constexpr bool FLAT = VEC == 1;
+    const uint8_t* mask;
+    const char* src;        // this lane's row (FLAT: the group's first) of the next group
+    int T, chunks, depth, slot, step;
+    int row;                // the lane's row of the next group to ask for
+    size_t step_bytes;
+    uint32_t base;
+    int in, use;            // bytes from base
+    unsigned lives;         // whether the lane's row counts, in the groups asked for: newest in bit 0
+    bool live;              // in the next one
+
+    __device__ __forceinline__ bool counts(int t) const { return t < T && (!mask || __ldg(mask + t)); }
+    __device__ __forceinline__ void start(const void* logits, const uint8_t* m, int T_, int E, int depth_, unsigned char* b,
+                                          int t0, int step_) {
+        const int lane = threadIdx.x & 31;
+        mask = m;
+        T = T_; depth = depth_; step = step_;
+        chunks = FLAT ? E * SIZE : E / VEC;  // FLAT: bytes of a row
+        slot = FLAT ? flat_bytes(RPW, E, SIZE) : NCH * 512;
+        base = smem_u32(b);
+        row = t0 + lane / LPR;
+        src = static_cast<const char*>(logits) + size_t(FLAT ? t0 : row) * (size_t(E) * SIZE);
+        step_bytes = size_t(step) * (size_t(E) * SIZE);
+        in = use = 0;
+        lives = 0;
+        live = counts(row);
+        for (int i = 0; i + 1 < depth; ++i) ask();
     }
-    __device__ __forceinline__ void start(const void* logits, const uint8_t* mask, long long t, long long step, int T, int E,
-                                          int l) {
-        live = counts(mask, t, T);
-        live2 = counts(mask, t + step, T);
-        next.load(logits, size_t(t) * E, E, l, live);
+    // One group of copies (nothing of rows that do not count); the mask bytes of the one behind it.
+    __device__ __forceinline__ void ask() {
+        const int lane = threadIdx.x & 31, l = lane % LPR;
+        const uint32_t dst = base + in + 16 * lane;
+        if constexpr (FLAT) {
+            if (__any_sync(FULL, live)) {
+                const int off = int(reinterpret_cast<uintptr_t>(src) & 15u), rows = min(RPW, T - (row - lane / LPR));
+                const int bytes = off + rows * chunks;
+                const char* from = src - off + 16 * lane;
+                for (int i = 16 * lane, d = 0; i < bytes; i += 512, d += 512)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                 :: "r"(dst + d), "l"(from + d), "r"(min(bytes - i, 16)) : "memory");
+            }
+        } else if (live) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+                if (l + LPR * i < chunks)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 :: "r"(dst + 512 * i), "l"(src + 16 * (l + LPR * i)) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in = in + slot == depth * slot ? 0 : in + slot;
+        lives = (lives << 1) | (live ? 1u : 0u);
+        src += step_bytes;
+        row += step;
+        live = counts(row);
     }
-    // Row t's values into v, and on; whether any of the warp's rows is to be looked at.
-    __device__ __forceinline__ bool take(const void* logits, const uint8_t* mask, long long t, long long step, int T, int E,
-                                         int l, float2 (&v)[NCH * VEC / 2]) {
-        const bool now = __any_sync(FULL, live);
-        next.get(v);
-        live = live2;
-        live2 = counts(mask, t + 2 * step, T);
-        next.load(logits, size_t(t + step) * E, E, l, live);
-        return now;
+    // Ask for one more group and wait for the oldest: its values, -infinity beyond the columns and in
+    // rows that do not count. Returns whether any of the warp's rows does.
+    __device__ __forceinline__ bool take(const void* logits, int t0, int E, float2 (&v)[NCH * VEC / 2], bool& now) {
+        const int lane = threadIdx.x & 31, l = lane % LPR;
+        ask();
+        if (depth == 6) asm volatile("cp.async.wait_group 5;" ::: "memory");
+        else if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        now = (lives >> (depth - 1)) & 1u;
+        const uint32_t at = base + use;
+        use = use + slot == depth * slot ? 0 : use + slot;
+        if (!__any_sync(FULL, now)) return false;
+        const float none = __uint_as_float(0xff800000u);
+        if constexpr (FLAT) {
+            __syncwarp();
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(logits) + size_t(t0) * (size_t(E) * SIZE)) & 15u;
+            const uint32_t r = at + off + (lane / LPR) * chunks;
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int c = l + LPR * i;
+                float x = none;
+                if (now && c < E) {
+                    if constexpr (DT == DT_F32) {
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(r + 4 * c) : "memory");
+                    } else {
+                        uint16_t u;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(r + 2 * c) : "memory");
+                        x = bf16f(u);
+                    }
+                }
+                if (i & 1) v[i / 2].y = x;
+                else v[i / 2].x = x;
+            }
+            __syncwarp();  // the slot has been read
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                constexpr uint32_t NONE = DT == DT_F32 ? 0xff800000u : 0xff80ff80u;
+                uint4 w = make_uint4(NONE, NONE, NONE, NONE);
+                if (now && l + LPR * i < chunks)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at + 16 * lane + 512 * i) : "memory");
+                if constexpr (VEC == 4) {
+                    v[2 * i] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+                    v[2 * i + 1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+                } else {
+                    v[4 * i] = make_float2(bf16lo(w.x), bf16hi(w.x));
+                    v[4 * i + 1] = make_float2(bf16lo(w.y), bf16hi(w.y));
+                    v[4 * i + 2] = make_float2(bf16lo(w.z), bf16hi(w.z));
+                    v[4 * i + 3] = make_float2(bf16lo(w.w), bf16hi(w.w));
+                }
+            }
+        }
+        return true;
     }
 };
 
@@ -168,6 +232,7 @@ struct BalanceParams {
     float* ws_prob;
     int32_t* ws_counts;
     Tail* ws_tail;
+    int depth, ring_bytes;  // of a warp's ring
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -192,20 +257,24 @@ __device__ __forceinline__ uint32_t peer_u32(uint32_t a) {
 template <int DT, int VEC, int NCH, int LPR, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_forward_kernel(const BalanceParams p) {
     constexpr int N2 = NCH * VEC / 2, THREADS = 32 * WARPS, RPW = 32 / LPR;  // pairs of a lane, rows of a warp
+    // the warps' rings; behind the last row cols [WARPS][E], whose first row becomes the block's sums
     extern __shared__ __align__(16) float sm[];
-    float* cols = sm;                                         // [WARPS][E]; then [E]: the block's
-    int* hist = reinterpret_cast<int*>(cols + WARPS * p.E);   // [E]
+    float* cols = sm;
+    __shared__ int hist[MAX_EXPERTS];
     __shared__ double zsum[WARPS];
     __shared__ int nsum[WARPS];
     __shared__ Tail tail;
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
-    const long long step = (long long)gridDim.x * WARPS * RPW;
-    long long t0 = ((long long)blockIdx.x * WARPS + warp) * RPW;  // the warp's first row, then this lane's
-    long long t = t0 + lane / LPR;
-    Walk<DT, VEC, NCH, LPR> walk;
-    walk.start(p.logits, p.mask, t, step, p.T, p.E, l);
+    // T is at most 2^30, and rows are asked for at most six steps (a step: 2^15 rows) beyond it
+    const int step = gridDim.x * WARPS * RPW;
+    int t0 = (blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;  // the warp's first row, and this lane's
+    Ring<DT, VEC, NCH, LPR> ring;
+    ring.start(p.logits, p.mask, p.T, p.E, p.depth, reinterpret_cast<unsigned char*>(sm) + warp * p.ring_bytes, t0, step);
     for (int e = threadIdx.x; e < p.E; e += THREADS) hist[e] = 0;
+    const int32_t* ids = p.ids + size_t(t) * p.k + l;
+    const size_t ids_step = size_t(step) * p.k;
+    int id_next = t < p.T && l < p.k ? __ldg(ids) : -1;
     __syncthreads();
 
     float2 acc[N2];
@@ -214,27 +283,30 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
     float z2 = 0.0f;
     int rows = 0;
     for (; t0 < p.T; t0 += step, t += step) {
-        int id = -1;
-        if (walk.live && l < p.k) id = __ldg(p.ids + size_t(t) * p.k + l);
+        const int id = id_next;
+        ids += ids_step;
+        id_next = t + step < p.T && l < p.k ? __ldg(ids) : -1;
+        bool now;
         float2 v[N2];
-        if (!walk.take(p.logits, p.mask, t, step, p.T, p.E, l, v)) continue;
+        if (!ring.take(p.logits, t0, p.E, v, now)) continue;
         float z;
         bool any;
         const float m = row_exp<N2, LPR>(v, z, any);
-        const float inv = any ? __fdividef(1.0f, z) : 0.0f;
+        const float inv = any ? rcp(z) : 0.0f;
 #pragma unroll
         for (int i = 0; i < N2; ++i) acc[i] = __ffma2_rn(v[i], all2(inv), acc[i]);
         if (any) {
-            const float lse = m + __logf(z);
+            const float lse = fmaf(lg2(z), LN2, m);
             z2 = fmaf(lse, lse, z2);
             ++rows;
             if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
             for (int j = l + LPR; j < p.k; j += LPR) {
-                id = __ldg(p.ids + size_t(t) * p.k + j);
-                if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+                const int more = __ldg(p.ids + size_t(t) * p.k + j);
+                if (more >= 0 && more < p.E) atomicAdd(&hist[more], 1);
             }
         }
     }
+    __syncthreads();  // the rings are done with
     // the warp's groups: columns, squares and rows (equal in all lanes of a group)
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
@@ -266,13 +338,15 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
         for (int w = 0; w < WARPS; ++w) s += cols[w * p.E + e];
         cols[e] = s;  // this thread's column only
     }
-    if (threadIdx.x == 0) {
-        Tail u{0.0, 0, 0};
-        for (int w = 0; w < WARPS; ++w) {
-            u.z += zsum[w];
-            u.rows += nsum[w];
+    if (warp == 0) {
+        double z = lane < WARPS ? zsum[lane] : 0.0;
+        int n = lane < WARPS ? nsum[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            z += __shfl_xor_sync(FULL, z, o);
+            n += __shfl_xor_sync(FULL, n, o);
         }
-        tail = u;
+        if (lane == 0) tail = Tail{z, n, 0};
     }
     // the cluster's sums, in block order: each of its blocks adds a share of the columns
     cluster_sync();
@@ -304,20 +378,24 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
     __syncthreads();
     if (!last) return;
     __threadfence();
-    if (threadIdx.x == 0) {
-        *p.ticket = 0;
+    if (warp == 0) {
         double z = 0.0;
-        long long n = 0;
-        for (int b = 0; b < clusters; ++b) {
+        int n = 0;
+        for (int b = lane; b < clusters; b += 32) {
             z += __ldcg(&p.ws_tail[b].z);
             n += __ldcg(&p.ws_tail[b].rows);
         }
-        zsum[0] = z;
-        nsum[0] = int(n);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            z += __shfl_xor_sync(FULL, z, o);
+            n += __shfl_xor_sync(FULL, n, o);
+        }
+        if (lane == 0) {
+            *p.ticket = 0;
+            zsum[0] = z;
+            nsum[0] = n;
+        }
     }
-    __syncthreads();
-    const int n = nsum[0];
-    const float inv_n = n ? 1.0f / float(n) : 0.0f;
     // four columns a thread, several threads a column group: each adds every parts-th cluster
     const int quads = padded(p.E) / 4, parts = THREADS / quads;
     const int quad = threadIdx.x % quads, part = threadIdx.x / quads;
@@ -337,6 +415,8 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
         csum[threadIdx.x] = c;
     }
     __syncthreads();
+    const int n = nsum[0];
+    const float inv_n = n ? 1.0f / float(n) : 0.0f;
     float balance = 0.0f;
     for (int e = threadIdx.x; e < p.E; e += THREADS) {
         float s = 0.0f;
@@ -371,6 +451,7 @@ struct BalanceGradParams {
     const int32_t* n_rows;
     const float* grad;
     void* dlogits;
+    int depth, ring_bytes;
 };
 
 template <int DT, int VEC, int NCH, int LPR>
@@ -398,10 +479,11 @@ template <int DT, int VEC, int NCH, int LPR, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_backward_kernel(const BalanceGradParams p) {
     constexpr int N2 = NCH * VEC / 2, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
-    const long long step = (long long)gridDim.x * WARPS * RPW;
-    long long t0 = ((long long)blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;
-    Walk<DT, VEC, NCH, LPR> walk;
-    walk.start(p.logits, p.mask, t, step, p.T, p.E, l);
+    const int step = gridDim.x * WARPS * RPW;
+    int t0 = (blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;
+    extern __shared__ __align__(16) unsigned char rings[];
+    Ring<DT, VEC, NCH, LPR> ring;
+    ring.start(p.logits, p.mask, p.T, p.E, p.depth, rings + warp * p.ring_bytes, t0, step);
     const int n = max(*p.n_rows, 1);
     const int mean = int((long long)n * p.k / p.E);
     const float gb = p.grad[0] * (float(p.E) / (float(n) * float(p.k))) / float(n);
@@ -416,7 +498,8 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_b
     }
     for (; t0 < p.T; t0 += step, t += step) {
         float2 v[N2];
-        if (walk.take(p.logits, p.mask, t, step, p.T, p.E, l, v)) {
+        bool now;
+        if (ring.take(p.logits, t0, p.E, v, now)) {
             float z;
             bool any;
             const float m = row_exp<N2, LPR>(v, z, any);
@@ -424,8 +507,8 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_b
 #pragma unroll
             for (int i = 0; i < N2; ++i) q = __ffma2_rn(v[i], f[i], q);
             // p (gb (f - s) + gz lse); nothing in rows that do not count, whose v is zero
-            const float inv = any ? __fdividef(1.0f, z) : 0.0f, s = row_sum<LPR>(q.x + q.y) * inv;
-            const float zt = any ? gz * (m + __logf(z)) * inv : 0.0f, a = gb * inv;
+            const float inv = any ? rcp(z) : 0.0f, s = row_sum<LPR>(q.x + q.y) * inv;
+            const float zt = any ? gz * fmaf(lg2(z), LN2, m) * inv : 0.0f, a = gb * inv;
 #pragma unroll
             for (int i = 0; i < N2; ++i)
                 v[i] = __fmul2_rn(v[i], __ffma2_rn(__fadd2_rn(f[i], all2(-s)), all2(a), all2(zt)));
@@ -458,9 +541,25 @@ int balance_blocks(int T, int rows, int most) {
     return need < 1 ? 1 : (need < most ? need : most);
 }
 
+// Depth of the rings in `room` bytes of shared memory (2, 3, 4 or 6 slots), and a ring's bytes.
+int ring_depth(int room, int E, int dtype, int* bytes) {
+    const int size = dtype == DT_F32 ? 4 : 2, rows = E <= 128 ? 4 : 1;
+    // rows of whole chunks: the lanes' places, at most 16 columns (E <= 128) or E / 32 rounded up to a
+    // power of two each
+    int slot = flat_bytes(rows, E, size);
+    if (E * size % 16 == 0) {
+        const int values = dtype == DT_F32 ? (E <= 32 ? 4 : E <= 128 ? 16 : E <= 256 ? 8 : E <= 512 ? 16 : 32)
+                                           : (E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 8 : E <= 512 ? 16 : 32);
+        slot = 32 * values * size;
+    }
+    const int fits = room / BAL_WARPS / slot;
+    const int depth = fits >= 6 ? 6 : (fits >= 4 ? 4 : (fits == 3 ? 3 : 2));
+    *bytes = depth * slot;
+    return depth;
+}
+
 // 16-byte chunks where every row starts on one, else single values; eight lanes a row up to 128
 // columns; the smallest number of chunks a lane needs.
-constexpr int BAL_WARPS = 16;
 int rows_a_block(int E) { return E <= 128 ? 4 * BAL_WARPS : BAL_WARPS; }
 
 #define BALANCE_PICK(kernel)                                                                              \
@@ -537,8 +636,13 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     p.ws_counts = reinterpret_cast<int32_t*>(base + w.counts);
     p.ws_tail = reinterpret_cast<Tail*>(base + w.tail);
     const ForwardKernel kern = pick_forward(logits_dtype, E);
-    const int sums = 4 * (BAL_WARPS + 1) * E, ends = 32 * 32 * BAL_WARPS;  // columns and counts; the last block's
-    const int smem = sums > ends ? sums : ends;                    // E = 1024: 69,632 bytes
+    // two blocks an SM (one above 512 columns), less their static part
+    const int room = di.max_smem_optin / (E <= 512 ? 2 : 1) - 8 * 1024;
+    p.depth = ring_depth(room, E, logits_dtype, &p.ring_bytes);
+    int smem = p.ring_bytes * BAL_WARPS;
+    const int sums = 4 * BAL_WARPS * E, ends = 32 * 32 * BAL_WARPS;  // columns; the last block's
+    smem = smem > sums ? smem : sums;
+    smem = smem > ends ? smem : ends;
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return REDMOE_ERR_CUDA;
@@ -583,8 +687,13 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     p.n_rows = n_rows;
     p.grad = grad_loss;
     p.dlogits = dlogits;
-    pick_backward(logits_dtype, E)<<<balance_blocks(T, rows_a_block(E), 2 * di.sm_count), 32 * BAL_WARPS, 0,
-                                     static_cast<cudaStream_t>(stream)>>>(p);
+    p.depth = ring_depth(di.max_smem_optin / (E <= 512 ? 2 : 1) - 2 * 1024, E, logits_dtype, &p.ring_bytes);
+    const int smem = p.ring_bytes * BAL_WARPS;
+    const BackwardKernel kern = pick_backward(logits_dtype, E);
+    if (smem > 40 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return REDMOE_ERR_CUDA;
+    kern<<<balance_blocks(T, rows_a_block(E), 2 * di.sm_count), 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 

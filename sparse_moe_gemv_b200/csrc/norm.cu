@@ -143,11 +143,11 @@ __device__ __forceinline__ void clear_unused(float* a, float* b, int n, int lane
         if (i % 16 >= tpr / 32) a[i] = b[i] = 0.0f;
 }
 
-// 1 / (1 + e^-a). The fast exponential is off by about 2 + 1.2 |a| units of e^-a, so by that much
-// only where e^-a decides (a < 0), 3 units in all at |a| = 1 and 14 at a = -10; the accurate one
-// and an IEEE divide cost 20 instructions more an element (the wide gated case: 134 against 96 us
-// together with packed arithmetic).
-__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
+// 1 / (1 + e^-a) with e^-a = 2^(-a log2 e): rounding the exponent makes e^-a off by about |a| units,
+// so the result only where e^-a decides (a < 0): 3 units in all at |a| = 1, 12 at a = -10. Four
+// instructions an element, two of them of the unit for special functions; expf and an IEEE divide
+// take some twenty more.
+__device__ __forceinline__ float sigmoid(float a) { return rcp(1.0f + ex2(a * -LOG2E)); }
 __device__ __forceinline__ F8 sigmoid(const F8& a) {
     F8 r;
 #pragma unroll

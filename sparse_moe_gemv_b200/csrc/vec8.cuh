@@ -19,6 +19,25 @@ __device__ __forceinline__ uint4 ld_row(const void* p) {
     return v;
 }
 
+// Powers and logarithms to the base of two and reciprocals as one instruction each, off by one or
+// two units; results below the smallest normal number are zero.
+__device__ __forceinline__ float ex2(float a) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+__device__ __forceinline__ float lg2(float a) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+__device__ __forceinline__ float rcp(float a) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
+
 // Eight fp32 values as pairs: one packed instruction works on two.
 struct F8 {
     float2 v[4];

@@ -18,10 +18,11 @@
 // a row is short (up to 128 columns), a lane the same columns of every row, so the column sums of P
 // stay in registers until the warp's rows are done. Rows are copied ahead into a ring of the warp's
 // in shared memory as the flat byte range that they are, whole 16-byte pieces whatever E is (short
-// and 16-bit rows need several in flight for full bandwidth). Forward, the
-// blocks of a cluster add their sums through distributed shared memory, and the last block to
-// finish adds the clusters': a single launch. Sums over rows are made in a fixed order (lane,
-// warp, block, cluster), counts are integers: results do not depend on timing.
+// and 16-bit rows need several in flight for full bandwidth). Forward, every block leaves its sums in
+// the workspace and a second kernel, one cluster that waits where the first one ends, adds them: the
+// last block of the first kernel doing that took 6 to 10 us behind fences and a counter, this takes
+// 3. Sums over rows are made in a fixed order (lane, warp, block), counts are integers: results do
+// not depend on timing.
 #include "common.cuh"
 #include "internal.h"
 #include "vec8.cuh"
@@ -30,8 +31,8 @@ namespace redmoe {
 namespace {
 
 constexpr int BAL_WARPS = 16;
-constexpr int BAL_CLUSTER = 4;
-constexpr int BAL_MAX_CLUSTERS = 80;  // two blocks an SM, 160 SMs
+constexpr int BAL_CLUSTER = 8;         // blocks of the second kernel
+constexpr int BAL_MAX_BLOCKS = 2 * 160;  // of the first: two an SM
 __host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }  // a row of sums in the workspace
 
 // A row lies over its LPR lanes in chunks of VEC consecutive values, chunk l + LPR i for lane l. VEC > 1
@@ -198,18 +199,17 @@ struct Ring {
     }
 };
 
-// Workspace: the control block, whose word 8 counts the blocks that are done, then per cluster
-// its column sums [E], its counts [E] and {sum of lse^2 (double), rows}.
+// Workspace: the control block (not used), then per block of the first kernel its column sums [E],
+// its counts [E] and {sum of lse^2, rows}.
 struct BalanceWs {
     size_t prob, counts, tail, total;
 };
-constexpr int TICKET_WORD = 8;
-BalanceWs balance_layout(int E) {
+BalanceWs balance_layout(int blocks, int E) {
     BalanceWs w;
     size_t o = 256;
-    w.prob = o; o = align256(o + 4ull * BAL_MAX_CLUSTERS * padded(E));
-    w.counts = o; o = align256(o + 4ull * BAL_MAX_CLUSTERS * padded(E));
-    w.tail = o; o = align256(o + 16ull * BAL_MAX_CLUSTERS);
+    w.prob = o; o = align256(o + 4ull * blocks * padded(E));
+    w.counts = o; o = align256(o + 4ull * blocks * padded(E));
+    w.tail = o; o = align256(o + 16ull * blocks);
     w.total = o;
     return w;
 }
@@ -228,31 +228,12 @@ struct BalanceParams {
     int32_t* counts;
     float* prob;
     int32_t* n_rows;
-    unsigned* ticket;
     float* ws_prob;
     int32_t* ws_counts;
     Tail* ws_tail;
+    int blocks;             // of the first kernel
     int depth, ring_bytes;  // of a warp's ring
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_addr(const void* p, int rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ uint32_t peer_u32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
 
 template <int DT, int VEC, int NCH, int LPR, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_forward_kernel(const BalanceParams p) {
@@ -263,8 +244,6 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
     __shared__ int hist[MAX_EXPERTS];
     __shared__ double zsum[WARPS];
     __shared__ int nsum[WARPS];
-    __shared__ Tail tail;
-    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
     // T is at most 2^30, and rows are asked for at most six steps (a step: 2^15 rows) beyond it
     const int step = gridDim.x * WARPS * RPW;
@@ -275,6 +254,7 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
     const int32_t* ids = p.ids + size_t(t) * p.k + l;
     const size_t ids_step = size_t(step) * p.k;
     int id_next = t < p.T && l < p.k ? __ldg(ids) : -1;
+    asm volatile("griddepcontrol.launch_dependents;");  // the second kernel may take its place to wait
     __syncthreads();
 
     float2 acc[N2];
@@ -336,7 +316,8 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) s += cols[w * p.E + e];
-        cols[e] = s;  // this thread's column only
+        p.ws_prob[size_t(blockIdx.x) * padded(p.E) + e] = s;
+        p.ws_counts[size_t(blockIdx.x) * padded(p.E) + e] = hist[e];
     }
     if (warp == 0) {
         double z = lane < WARPS ? zsum[lane] : 0.0;
@@ -346,101 +327,114 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
             z += __shfl_xor_sync(FULL, z, o);
             n += __shfl_xor_sync(FULL, n, o);
         }
-        if (lane == 0) tail = Tail{z, n, 0};
+        if (lane == 0) p.ws_tail[blockIdx.x] = Tail{z, n, 0};
     }
-    // the cluster's sums, in block order: each of its blocks adds a share of the columns
-    cluster_sync();
-    const int rank = cluster_rank(), cluster = blockIdx.x / BAL_CLUSTER, clusters = gridDim.x / BAL_CLUSTER;
-    for (int e = rank * THREADS + threadIdx.x; e < p.E; e += BAL_CLUSTER * THREADS) {
-        float s = 0.0f;
-        int c = 0;
-#pragma unroll
-        for (int r = 0; r < BAL_CLUSTER; ++r) {
-            s += __uint_as_float(peer_u32(peer_addr(cols + e, r)));
-            c += int(peer_u32(peer_addr(hist + e, r)));
-        }
-        p.ws_prob[size_t(cluster) * padded(p.E) + e] = s;
-        p.ws_counts[size_t(cluster) * padded(p.E) + e] = c;
-    }
-    if (rank == 0 && threadIdx.x == 0) {
-        Tail u{0.0, 0, 0};
-        for (int r = 0; r < BAL_CLUSTER; ++r) {
-            const uint32_t a = peer_addr(&tail, r);
-            u.z += __hiloint2double(int(peer_u32(a + 4)), int(peer_u32(a)));
-            u.rows += int(peer_u32(a + 8));
-        }
-        p.ws_tail[cluster] = u;
-    }
-    // the block that is last to finish adds the clusters' sums, in cluster order
-    __threadfence();
-    cluster_sync();  // no block leaves while another reads its shared memory
-    if (threadIdx.x == 0) last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    if (warp == 0) {
-        double z = 0.0;
-        int n = 0;
-        for (int b = lane; b < clusters; b += 32) {
-            z += __ldcg(&p.ws_tail[b].z);
-            n += __ldcg(&p.ws_tail[b].rows);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            z += __shfl_xor_sync(FULL, z, o);
-            n += __shfl_xor_sync(FULL, n, o);
-        }
-        if (lane == 0) {
-            *p.ticket = 0;
-            zsum[0] = z;
-            nsum[0] = n;
-        }
-    }
-    // four columns a thread, several threads a column group: each adds every parts-th cluster
-    const int quads = padded(p.E) / 4, parts = THREADS / quads;
-    const int quad = threadIdx.x % quads, part = threadIdx.x / quads;
-    float4* fsum = reinterpret_cast<float4*>(cols);             // [parts][quads], at most THREADS
-    int4* csum = reinterpret_cast<int4*>(fsum + THREADS);
-    if (part < parts) {
-        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        int4 c = make_int4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int b = part; b < clusters; b += parts) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_prob) + size_t(b) * quads + quad);
-            const int4 u = __ldcg(reinterpret_cast<const int4*>(p.ws_counts) + size_t(b) * quads + quad);
+}
+
+// The second kernel: rank r of the cluster adds the blocks' sums of its share of the columns, every
+// thread four columns of every parts-th block, then the parts in order; rank 0 makes the losses.
+constexpr int FIN_THREADS = 1024;
+__global__ void __cluster_dims__(BAL_CLUSTER, 1, 1) __launch_bounds__(FIN_THREADS) balance_finish_kernel(const BalanceParams p) {
+    __shared__ float4 fsum[FIN_THREADS];
+    __shared__ int4 csum[FIN_THREADS];
+    __shared__ double zsum[32];
+    __shared__ int nsum[32];
+    __shared__ double part_loss;
+    __shared__ double wsum[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int quads = padded(p.E) / 4, share = (quads + BAL_CLUSTER - 1) / BAL_CLUSTER;  // 1 .. 32 column groups
+    const int q0 = int(rank) * share, mine = max(0, min(share, quads - q0));
+    const int parts = FIN_THREADS / share, quad = threadIdx.x % share, part = threadIdx.x / share;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int4 c = make_int4(0, 0, 0, 0);
+    if (part < parts && quad < mine) {
+#pragma unroll 4
+        for (int b = part; b < p.blocks; b += parts) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_prob) + size_t(b) * quads + q0 + quad);
+            const int4 u = __ldcg(reinterpret_cast<const int4*>(p.ws_counts) + size_t(b) * quads + q0 + quad);
             f.x += v.x; f.y += v.y; f.z += v.z; f.w += v.w;
             c.x += u.x; c.y += u.y; c.z += u.z; c.w += u.w;
         }
-        fsum[threadIdx.x] = f;
-        csum[threadIdx.x] = c;
+    }
+    fsum[threadIdx.x] = f;
+    csum[threadIdx.x] = c;
+    double z = 0.0;
+    int n = 0;
+    if (threadIdx.x < p.blocks) {  // at most BAL_MAX_BLOCKS < FIN_THREADS
+        z = __ldcg(&p.ws_tail[threadIdx.x].z);
+        n = __ldcg(&p.ws_tail[threadIdx.x].rows);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        z += __shfl_xor_sync(FULL, z, o);
+        n += __shfl_xor_sync(FULL, n, o);
+    }
+    if (lane == 0) {
+        zsum[warp] = z;
+        nsum[warp] = n;
     }
     __syncthreads();
-    const int n = nsum[0];
+    z = zsum[lane];
+    n = nsum[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        z += __shfl_xor_sync(FULL, z, o);
+        n += __shfl_xor_sync(FULL, n, o);
+    }
     const float inv_n = n ? 1.0f / float(n) : 0.0f;
-    float balance = 0.0f;
-    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    // eight threads a column: parts h, h + 8, ... each, then the eight
+    double balance = 0.0;
+    {
+        const int col = threadIdx.x >> 3, h = threadIdx.x & 7;  // at most 128 columns a block
         float s = 0.0f;
-        int c = 0;
-        for (int i = 0; i < parts; ++i) {
-            s += reinterpret_cast<const float*>(fsum + i * quads)[e];
-            c += reinterpret_cast<const int*>(csum + i * quads)[e];
+        int m = 0;
+        if (col < 4 * mine) {
+            for (int i = h; i < parts; i += 8) {
+                s += reinterpret_cast<const float*>(fsum + i * share)[col];
+                m += reinterpret_cast<const int*>(csum + i * share)[col];
+            }
         }
-        s *= inv_n;
-        p.prob[e] = s;
-        p.counts[e] = c;
-        balance = fmaf(float(c), s, balance);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(FULL, s, o);
+            m += __shfl_xor_sync(FULL, m, o);
+        }
+        const int e = 4 * q0 + col;
+        if (h == 0 && col < 4 * mine && e < p.E) {
+            p.prob[e] = s * inv_n;
+            p.counts[e] = m;
+            balance = double(m) * double(s * inv_n);
+        }
     }
-    __syncthreads();  // the sums have been read
-    balance = warp_sum(balance);
-    if (lane == 0) cols[warp] = balance;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) balance += __shfl_xor_sync(FULL, balance, o);
+    if (lane == 0) wsum[warp] = balance;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
+        balance = wsum[lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) balance += __shfl_xor_sync(FULL, balance, o);
+        if (lane == 0) part_loss = balance;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0 && threadIdx.x == 0) {
         double s = 0.0;
-        for (int w = 0; w < WARPS; ++w) s += cols[w];
+        for (int r = 0; r < BAL_CLUSTER; ++r) {
+            uint32_t a;
+            double v;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&part_loss)), "r"(r));
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
+            s += v;
+        }
         p.loss[0] = n ? float(s * p.E / (double(n) * p.k)) : 0.0f;
-        p.loss[1] = n ? float(zsum[0] / n) : 0.0f;
+        p.loss[1] = n ? float(z / n) : 0.0f;
         *p.n_rows = n;
     }
+    // no block leaves while rank 0 reads its shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 struct BalanceGradParams {
@@ -593,7 +587,7 @@ extern "C" {
 
 size_t redmoe_balance_workspace_bytes(int32_t T, int32_t E) {
     if (T < 0 || E <= 0 || E > MAX_EXPERTS) return 0;
-    return balance_layout(E).total;
+    return balance_layout(balance_blocks(T, rows_a_block(E), BAL_MAX_BLOCKS), E).total;
 }
 
 redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, const int32_t* topk_ids,
@@ -620,7 +614,10 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     }
     DevInfo di;
     if (!get_dev_info(&di)) return REDMOE_ERR_CUDA;
-    const BalanceWs w = balance_layout(E);
+    // two blocks an SM (one above 512 columns)
+    const int each = E <= 512 ? 2 : 1, most = each * di.sm_count;
+    const int blocks = balance_blocks(T, rows_a_block(E), most < BAL_MAX_BLOCKS ? most : BAL_MAX_BLOCKS);
+    const BalanceWs w = balance_layout(blocks, E);
     char* base = static_cast<char*>(workspace);
     BalanceParams p;
     p.logits = logits;
@@ -631,37 +628,30 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     p.counts = counts;
     p.prob = prob;
     p.n_rows = n_rows;
-    p.ticket = reinterpret_cast<unsigned*>(base) + TICKET_WORD;
+    p.blocks = blocks;
     p.ws_prob = reinterpret_cast<float*>(base + w.prob);
     p.ws_counts = reinterpret_cast<int32_t*>(base + w.counts);
     p.ws_tail = reinterpret_cast<Tail*>(base + w.tail);
     const ForwardKernel kern = pick_forward(logits_dtype, E);
-    // two blocks an SM (one above 512 columns), less their static part
-    const int room = di.max_smem_optin / (E <= 512 ? 2 : 1) - 8 * 1024;
-    p.depth = ring_depth(room, E, logits_dtype, &p.ring_bytes);
+    p.depth = ring_depth(di.max_smem_optin / each - 8 * 1024, E, logits_dtype, &p.ring_bytes);  // less the static part
     int smem = p.ring_bytes * BAL_WARPS;
-    const int sums = 4 * BAL_WARPS * E, ends = 32 * 32 * BAL_WARPS;  // columns; the last block's
+    const int sums = 4 * BAL_WARPS * E;
     smem = smem > sums ? smem : sums;
-    smem = smem > ends ? smem : ends;
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return REDMOE_ERR_CUDA;
-    // whole clusters lie in one GPC each: about 24 of 25 places can be had
-    const int places = di.sm_count * (E <= 512 ? 2 : 1) / BAL_CLUSTER * 24 / 25;
-    const int most = places < 1 ? 1 : (places < BAL_MAX_CLUSTERS ? places : BAL_MAX_CLUSTERS);
-    const int clusters = balance_blocks(T, rows_a_block(E) * BAL_CLUSTER, most);
+    kern<<<blocks, 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(clusters * BAL_CLUSTER);
-    cfg.blockDim = dim3(32 * BAL_WARPS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3(BAL_CLUSTER);
+    cfg.blockDim = dim3(FIN_THREADS);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = BAL_CLUSTER;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, balance_finish_kernel, p) == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, const uint8_t* row_mask, int32_t T,

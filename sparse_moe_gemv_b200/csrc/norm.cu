@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
         }
     }
     if (!p.part) return;
+    asm volatile("griddepcontrol.launch_dependents;");  // norm_columns_kernel may take its place to wait
     // the groups' column sums, added in group order by group 0
     __syncthreads();
     if (group > 0) {
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, i
     const int which = blockIdx.y, q = threadIdx.x & 7, slice = threadIdx.x >> 3;
     if (which == 0 ? !dpre : !(dpost || dgate)) return;
     const int col = blockIdx.x * 32 + 4 * q;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (col < p.H) {
         const float* src = p.part + size_t(which) * p.H + col;
@@ -785,9 +787,18 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     kern<<<blocks, threads, smem, stm>>>(p);
     if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
     if (!work) return REDMOE_OK;
-    norm_columns_kernel<<<dim3((p.H + 31) / 32, 2), 256, 0, stm>>>(p, blocks, dpre_w, dpost_w,
-                                                                   p.want_gate ? static_cast<float*>(dgate) : nullptr);
-    return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((p.H + 31) / 32, 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stm;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_columns_kernel, p, blocks, dpre_w, dpost_w,
+                                             p.want_gate ? static_cast<float*>(dgate) : static_cast<float*>(nullptr));
+    return e == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -45,11 +45,9 @@ namespace {
 
 constexpr int GV_MAX_T = 32;
 constexpr int GV_MAX_K = 65536;
-constexpr int GV_COLS = 256;     // columns of a step
+constexpr int GV_COLS = 256;     // columns of a slice, the unit of x's layout
 constexpr int GV_PAD = 64;       // bytes between token rows of x in shared memory (bank offset)
 constexpr int GV_ZERO = 256;     // bytes of zeros: half a step of an absent token
-constexpr int GV_WROW = GV_COLS / 2 + 16;                  // bytes of a slot's row of W (bank offset)
-constexpr int GV_SROW = GV_COLS / 16;                      // bytes of a slot's row of scales
 
 struct GemvParams {
     const uint8_t* w;      // [N, K/2]
@@ -183,9 +181,12 @@ template <int NT> struct Plan {
     static constexpr int M = NT == 1 ? 2 : 1;       // tiles of 16 rows in a step: x is read once for them
     static constexpr int WARPS = ONE ? 20 : 16;                    // at most
     static constexpr int ROWS = 16 * M;
+    static constexpr int COLS = ONE ? 512 : 256;    // columns of a step: one or two slices
+    static constexpr int WROW = COLS / 2 + 16;      // bytes of a slot's row of W (bank offset)
+    static constexpr int SROW = COLS / 16;          // bytes of a slot's row of scales
     static constexpr int NA = M * 4 * (ONE ? 1 : NT);              // sums a lane holds
-    static constexpr int SLOTS = 3;                                // of a warp's ring
-    static constexpr int SLOT = ROWS * (GV_WROW + GV_SROW);
+    static constexpr int SLOTS = ONE ? 2 : 3;                      // of a warp's ring
+    static constexpr int SLOT = ROWS * (WROW + SROW);
     static constexpr int WARP_BYTES = SLOTS * SLOT + NA * 32 * 4;  // shared memory of a warp
     static constexpr int fixed_bytes(int T, int K) {               // and of a block besides
         return T * row_stride(K) + GV_ZERO + 128 + 128 + 4 * 8 * (ONE ? TOK : 2 * TOK) * ((K + GV_COLS - 1) / GV_COLS);
@@ -194,51 +195,59 @@ template <int NT> struct Plan {
 
 // Position in a warp's share of steps, with the lane's first address there: eight lanes read 128
 // bytes of a row, lane l chunk l % 8 of rows l / 8 + 4 j.
-template <int ROWS>
+template <class P>
 struct Cursor {
+    static constexpr int LANES = 32 / P::ROWS ? 32 / P::ROWS : 1;  // lanes that share a row's scales
     const uint8_t* w;
-    const uint16_t* sc;  // scales of row lane % ROWS
+    const uint16_t* sc;
     int tile, s;
     __device__ __forceinline__ void at(const GemvParams& p, int tile_, int s_, int lane) {
         tile = tile_;
         s = s_;
-        w = p.w + size_t(tile * ROWS + lane / 8) * (p.K / 2) + size_t(s) * (GV_COLS / 2) + 16 * (lane % 8);
-        sc = p.s + size_t(tile * ROWS + lane % ROWS) * (p.K / 32) + s * (GV_COLS / 32);
+        w = p.w + size_t(tile * P::ROWS + lane / 8) * (p.K / 2) + size_t(s) * (P::COLS / 2) + 16 * (lane % 8);
+        sc = p.s + size_t(tile * P::ROWS + lane % P::ROWS) * (p.K / 32) + s * (P::COLS / 32);
     }
     __device__ __forceinline__ void next(const GemvParams& p, int steps, int lane) {
-        w += GV_COLS / 2;
-        sc += GV_COLS / 32;
+        w += P::COLS / 2;
+        sc += P::COLS / 32;
         if (++s == steps) at(p, tile + 1, 0, lane);
     }
 };
 
 // Ask for one step. Rows beyond N and columns beyond K keep what the slot holds: any code is
-// finite and meets a zero x or an output that is not stored. Scales beyond K are zeroed (what
-// lies there need not be finite). WHOLE: K % 256 == 0, a row's scales of a step are 16 bytes.
-template <bool WHOLE, int ROWS>
-__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<ROWS>& c, int lane, unsigned char* slot) {
-    const uint32_t dst = smem_u32(slot) + (lane / 8) * GV_WROW + 16 * (lane % 8);
-    const int groups = p.K / 32 - c.s * (GV_COLS / 32);  // groups left in the row
+// finite and meets a zero x or an output that is not stored. Scales beyond K are not used (whole
+// slices) or zeroed: what lies there need not be finite. WHOLE: K % 256 == 0, a row's scales of a
+// slice are 16 bytes.
+template <bool WHOLE, class P>
+__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<P>& c, int lane, unsigned char* slot) {
+    constexpr int SLICES = P::COLS / GV_COLS;
+    const uint32_t dst = smem_u32(slot) + (lane / 8) * P::WROW + 16 * (lane % 8);
+    const int groups = p.K / 32 - c.s * (P::COLS / 32);  // groups left in the row
     const size_t step4 = size_t(p.K) * 2;                // bytes of four rows
-    if (WHOLE || lane % 8 < groups) {
-        if (c.tile * ROWS + ROWS <= p.N) {
+    const bool full = c.tile * P::ROWS + P::ROWS <= p.N;
 #pragma unroll
-            for (int j = 0; j < ROWS / 4; ++j) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
+    for (int h = 0; h < SLICES; ++h) {
+        if (WHOLE ? h > 0 && groups <= 8 * h : groups <= 8 * h + lane % 8) continue;
+        if (full) {
+#pragma unroll
+            for (int j = 0; j < P::ROWS / 4; ++j) cp_async16(dst + 4 * j * P::WROW + 128 * h, c.w + j * step4 + 128 * h);
         } else {
 #pragma unroll
-            for (int j = 0; j < ROWS / 4; ++j)
-                if (c.tile * ROWS + lane / 8 + 4 * j < p.N) cp_async16(dst + 4 * j * GV_WROW, c.w + j * step4);
+            for (int j = 0; j < P::ROWS / 4; ++j)
+                if (c.tile * P::ROWS + lane / 8 + 4 * j < p.N)
+                    cp_async16(dst + 4 * j * P::WROW + 128 * h, c.w + j * step4 + 128 * h);
         }
     }
-    unsigned char* ss = slot + ROWS * GV_WROW + (lane % ROWS) * GV_SROW;
-    if (c.tile * ROWS + lane % ROWS < p.N) {
+    unsigned char* ss = slot + P::ROWS * P::WROW + (lane % P::ROWS) * P::SROW;
+    if (full || c.tile * P::ROWS + lane % P::ROWS < p.N) {
+        const int h = lane / P::ROWS;  // the lanes that share a row take a slice each
         if (WHOLE) {
-            if (lane < ROWS) cp_async16(smem_u32(ss), c.sc);
+            if (h < SLICES && (h == 0 || groups > 8 * h)) cp_async16(smem_u32(ss) + 16 * h, c.sc + 8 * h);
         } else {
-            constexpr int EACH = 8 * ROWS / 32;  // scales a lane fetches
+            constexpr int EACH = P::COLS / 32 / Cursor<P>::LANES;  // scales a lane fetches
 #pragma unroll
             for (int i = 0; i < EACH; ++i) {
-                const int k = EACH * (lane / ROWS) + i;
+                const int k = EACH * h + i;
                 reinterpret_cast<uint16_t*>(ss)[k] = k < groups ? __ldg(c.sc + k) : uint16_t(0);
             }
         }
@@ -250,15 +259,15 @@ __device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<ROWS>& c
 // 2 q, 2 q + 1 of a lane's sums count where they are that half's.
 // w: the lane's first chunk, s: the first row's scales; `release` is called once they are read.
 // x: the lane's column of B (zeros in the lanes that hold other groups). gs: its two group sums.
-template <class Release>
+template <class P, class Release>
 __device__ __forceinline__ void one_step(const unsigned char* w, const unsigned char* s, Release release,
                                          const unsigned char* x, const float* gs, float (&acc)[4]) {
     uint4 v[4];
     uint32_t sc[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * GV_WROW);
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(w + 4 * j * P::WROW);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * GV_SROW);
+    for (int j = 0; j < 4; ++j) sc[j] = *reinterpret_cast<const uint32_t*>(s + 4 * j * P::SROW);
     release();
     float cc[2][4];
     const float2 c = *reinterpret_cast<const float2*>(gs);
@@ -285,17 +294,17 @@ __device__ __forceinline__ void one_step(const unsigned char* w, const unsigned 
 // Eight NT tokens, M tiles of 16 rows by 128 columns: lane (g, q) reads its quarter of the four
 // groups of rows g and g + 8; x holds the lane's token of each block of eight, gs the group sums
 // that the lane's part of C starts with in the first block.
-template <int NT, int M, class Release>
+template <class P, int NT, int M, class Release>
 __device__ __forceinline__ void row_step(const unsigned char* w, const unsigned char* s, Release release,
                                          const unsigned char* const (&x)[NT], const float* gs, float (&acc)[4 * NT * M]) {
     uint2 sc[2 * M];
     uint32_t w4[4][2 * M];
 #pragma unroll
-    for (int m = 0; m < 2 * M; ++m) sc[m] = *reinterpret_cast<const uint2*>(s + 8 * m * GV_SROW);
+    for (int m = 0; m < 2 * M; ++m) sc[m] = *reinterpret_cast<const uint2*>(s + 8 * m * P::SROW);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int m = 0; m < 2 * M; ++m) w4[i][m] = *reinterpret_cast<const uint32_t*>(w + 8 * m * GV_WROW + 16 * i);
+        for (int m = 0; m < 2 * M; ++m) w4[i][m] = *reinterpret_cast<const uint32_t*>(w + 8 * m * P::WROW + 16 * i);
     release();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -332,14 +341,14 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     using P = Plan<NT>;
     constexpr bool ONE = P::ONE;
     constexpr int TOK = P::TOK, NA = P::NA, ROWS = P::ROWS, RING = P::SLOTS * P::SLOT;
-    const int steps = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
+    const int steps = (p.K + P::COLS - 1) / P::COLS, slices = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int g = lane >> 2, q = lane & 3;
     unsigned char* xs = sm;
     unsigned char* zero = xs + size_t(p.T) * stride;
     int* exps = reinterpret_cast<int*>(zero + GV_ZERO);     // [TOK], in 128 bytes
-    float* gsum = reinterpret_cast<float*>(exps + 32);      // [TOK][8 steps] or [8 steps][2 TOK]
-    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + (ONE ? 1 : 2) * TOK * 8 * steps);  // 128 bytes
+    float* gsum = reinterpret_cast<float*>(exps + 32);      // [8 slices] or [8 slices][2 TOK]
+    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + (ONE ? 1 : 2) * TOK * 8 * slices);  // 128 bytes
     float* red = reinterpret_cast<float*>(tops + 32);                      // [warps][NA][32]
     unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * RING;
 
@@ -350,12 +359,12 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     auto begin = [&](int w) { return w * each + min(w, more); };
     const int za = begin(warp), zb = begin(warp + 1);
 
-    Cursor<ROWS> in;
+    Cursor<P> in;
     in.at(p, ta + za / steps, za % steps, lane);
     int tile = in.tile, s = in.s, zin = za, sin = 0;
     auto ask = [&]() {  // one group per call, an empty one behind the last step
         if (zin < zb) {
-            fetch<WHOLE, ROWS>(p, in, lane, ring + sin);
+            fetch<WHOLE, P>(p, in, lane, ring + sin);
             in.next(p, steps, lane);
             sin = sin + P::SLOT == RING ? 0 : sin + P::SLOT;
             ++zin;
@@ -378,10 +387,10 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     for (int i = 0; i < NX; ++i) {
         const bool there = ONE ? (g & 3) == q : 8 * i + g < p.T;  // one token: this lane is its column's group
         x0[i] = (there ? xs + (ONE ? 64 * g : (8 * i + g) * stride) : zero) + (ONE ? 0 : 16 * q);
-        xstep[i] = there ? 2 * GV_COLS : 0;
+        xstep[i] = there ? 2 * P::COLS : 0;
     }
-    const unsigned char* my_w = ring + (ONE ? (lane / 8) * GV_WROW + 16 * (lane % 8) : g * GV_WROW + 4 * q);
-    const unsigned char* my_s = ring + ROWS * GV_WROW + (ONE ? (lane / 8) * GV_SROW + 4 * q : g * GV_SROW);
+    const unsigned char* my_w = ring + (ONE ? (lane / 8) * P::WROW + 16 * (lane % 8) : g * P::WROW + 4 * q);
+    const unsigned char* my_s = ring + ROWS * P::WROW + (ONE ? (lane / 8) * P::SROW + 4 * q : g * P::SROW);
     const float* my_g = gsum + (ONE ? 2 : 4) * q;
 
     float acc[NA] = {};
@@ -425,14 +434,18 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
             ask();
         };
         if constexpr (ONE) {
-            one_step(w, sc, release, x0[0] + s * xstep[0], my_g + 8 * s, acc);
+            const unsigned char* x = x0[0] + s * xstep[0];
+            const float* gs = my_g + 16 * s;
+            const bool two = (2 * s + 1) * GV_COLS < p.K;
+            one_step<P>(w, sc, [&]() { if (!two) release(); }, x, gs, acc);
+            if (two) one_step<P>(w + 128, sc + 16, release, x + xstep[0] / 2, gs + 8, acc);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const unsigned char* xp[NX];
 #pragma unroll
                 for (int i = 0; i < NX; ++i) xp[i] = x0[i] + s * xstep[i] + h * (xstep[i] / 2);
-                row_step<NT, P::M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * (2 * TOK), acc);
+                row_step<P, NT, P::M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * (2 * TOK), acc);
             }
         }
         slot = slot + P::SLOT == RING ? 0 : slot + P::SLOT;

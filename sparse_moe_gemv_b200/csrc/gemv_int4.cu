@@ -371,7 +371,10 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
         }
         cp_commit();
     };
-        const RowShare share(p.T);
+        // launched while the kernel before it ends: nothing is read or written before that has ended
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const RowShare share(p.T);
     fetch_x(p, share, stride, xs);
     cp_commit();
 #pragma unroll
@@ -489,8 +492,17 @@ bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
     if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return false;
     const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
-    kern<<<tiles < di.sm_count ? tiles : di.sm_count, 32 * warps, smem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles < di.sm_count ? tiles : di.sm_count);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
 }
 
 // Whether T tokens of K columns leave room for eight warps' rings.

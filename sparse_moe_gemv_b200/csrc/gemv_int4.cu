@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t pow2_pair(int e) { return uint32_t(127 + e) 
 // Once this thread's part of fetch_x has arrived: x as B wants it. Every run of eight columns in
 // the order (0,4) (1,5)/16 (2,6) (3,7)/16, times 2^(GV_TOP - e) with e the exponent of the row's
 // largest element; exps[t] = e. gsum: -8 times the sum of each group in the units of the products
-// (ONE: [group], else [group][token pair] as the four numbers of C), made by the products themselves with a tile of
+// (ONE: [group], else [group][token]), made by the products themselves with a tile of
 // eights. tops: scratch, one word for each warp of each row.
 template <bool ONE, int TOK>
 __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh, int stride, unsigned char* xs, const unsigned char* zero,
@@ -167,7 +167,7 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
             if (ONE) {
                 if (t == 0) gsum[group] = -d[0];
             } else {
-                *reinterpret_cast<float4*>(gsum + 2 * (group * TOK + t)) = make_float4(-d[0], -d[1], -d[0], -d[1]);
+                *reinterpret_cast<float2*>(gsum + group * TOK + t) = make_float2(-d[0], -d[1]);
             }
         }
     }
@@ -185,11 +185,11 @@ template <int NT> struct Plan {
     static constexpr int WROW = COLS / 2 + 16;      // bytes of a slot's row of W (bank offset)
     static constexpr int SROW = COLS / 16;          // bytes of a slot's row of scales
     static constexpr int NA = M * 4 * (ONE ? 1 : NT);              // sums a lane holds
-    static constexpr int SLOTS = ONE ? 2 : 3;                      // of a warp's ring
+    static constexpr int SLOTS = NT == 2 ? 3 : 2;                  // of a warp's ring
     static constexpr int SLOT = ROWS * (WROW + SROW);
     static constexpr int WARP_BYTES = SLOTS * SLOT + NA * 32 * 4;  // shared memory of a warp
     static constexpr int fixed_bytes(int T, int K) {               // and of a block besides
-        return T * row_stride(K) + GV_ZERO + 128 + 128 + 4 * 8 * (ONE ? TOK : 2 * TOK) * ((K + GV_COLS - 1) / GV_COLS);
+        return T * row_stride(K) + GV_ZERO + 128 + 128 + 4 * 8 * TOK * ((K + GV_COLS - 1) / GV_COLS);
     }
 };
 
@@ -312,13 +312,13 @@ __device__ __forceinline__ void row_step(const unsigned char* w, const unsigned 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const uint4 xv = *reinterpret_cast<const uint4*>(x[nt] + 64 * i);
-            const float4 c = *reinterpret_cast<const float4*>(gs + i * (16 * NT) + 16 * nt);
+            const float2 c = *reinterpret_cast<const float2*>(gs + i * (8 * NT) + 8 * nt);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const uint32_t ua = i < 2 ? sc[2 * m].x : sc[2 * m].y, ub = i < 2 ? sc[2 * m + 1].x : sc[2 * m + 1].y;
                 const float fa = i & 1 ? bf16hi(ua) : bf16lo(ua), fb = i & 1 ? bf16hi(ub) : bf16lo(ub);
                 float cc[4];
-                mma_word(cc, v[2 * m], v[2 * m + 1], xv, c.x, c.y, c.z, c.w);
+                mma_word(cc, v[2 * m], v[2 * m + 1], xv, c.x, c.y, c.x, c.y);
                 float* to = acc + 4 * (m * NT + nt);
                 const float2 u = __ffma2_rn(make_float2(cc[0], cc[1]), make_float2(fa, fa), make_float2(to[0], to[1]));
                 const float2 v2 = __ffma2_rn(make_float2(cc[2], cc[3]), make_float2(fb, fb), make_float2(to[2], to[3]));
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     unsigned char* xs = sm;
     unsigned char* zero = xs + size_t(p.T) * stride;
     int* exps = reinterpret_cast<int*>(zero + GV_ZERO);     // [TOK], in 128 bytes
-    float* gsum = reinterpret_cast<float*>(exps + 32);      // [8 slices] or [8 slices][2 TOK]
-    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + (ONE ? 1 : 2) * TOK * 8 * slices);  // 128 bytes
+    float* gsum = reinterpret_cast<float*>(exps + 32);      // [8 slices] or [8 slices][TOK]
+    uint32_t* tops = reinterpret_cast<uint32_t*>(gsum + TOK * 8 * slices);  // 128 bytes
     float* red = reinterpret_cast<float*>(tops + 32);                      // [warps][NA][32]
     unsigned char* ring = reinterpret_cast<unsigned char*>(red + warps * NA * 32) + warp * RING;
 
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
     }
     const unsigned char* my_w = ring + (ONE ? (lane / 8) * P::WROW + 16 * (lane % 8) : g * P::WROW + 4 * q);
     const unsigned char* my_s = ring + ROWS * P::WROW + (ONE ? (lane / 8) * P::SROW + 4 * q : g * P::SROW);
-    const float* my_g = gsum + (ONE ? 2 : 4) * q;
+    const float* my_g = gsum + 2 * q;
 
     float acc[NA] = {};
     auto put_tile = [&](int tl, const float (&v)[NA]) {
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
                 const unsigned char* xp[NX];
 #pragma unroll
                 for (int i = 0; i < NX; ++i) xp[i] = x0[i] + s * xstep[i] + h * (xstep[i] / 2);
-                row_step<P, NT, P::M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * (2 * TOK), acc);
+                row_step<P, NT, P::M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * TOK, acc);
             }
         }
         slot = slot + P::SLOT == RING ? 0 : slot + P::SLOT;

@@ -363,8 +363,9 @@ redmoe_status redmoe_norm_forward(const redmoe_norm *N, const void *h, const voi
  *            not wanted
  *   dpost_w, dpre_w   fp32 [hidden], 16-byte aligned; NULL: not wanted
  * Overwritten, not accumulated; sums over rows are fp32 in a fixed order. The workspace is
- * needed for dpost_w, dpre_w and a CHANNEL dgate (else it may be NULL); its control block
- * is not used. T == 0 zeroes those three and touches nothing else. */
+ * needed for dpost_w, dpre_w and a CHANNEL dgate (else it may be NULL) and starts with the
+ * usual control block (zero before the first use, left zero). T == 0 zeroes those three and
+ * touches nothing else. */
 size_t redmoe_norm_workspace_bytes(const redmoe_norm *N, int32_t T);
 redmoe_status redmoe_norm_backward(const redmoe_norm *N, const void *h_out, const void *y, const void *gate,
                                    const void *dh_out, const void *dx, int32_t T, void *dh, void *dy, void *dgate,
@@ -405,8 +406,8 @@ redmoe_status redmoe_forward_block(const redmoe_layer *L, const redmoe_norm *bef
  * are those of the forward call. E is 1..1024, k 1..min(E, 32), T k at most 2^30; logits
  * REDMOE_F32 or REDMOE_BF16, 16-byte aligned. Sums over rows have a fixed order: results do
  * not depend on timing. Outputs must not overlap inputs or one another
- * (REDMOE_ERR_INVALID_ARG). The workspace holds redmoe_balance_workspace_bytes(T, E) bytes
- * and starts with the usual control block (zero before the first use, left zero). T == 0
+ * (REDMOE_ERR_INVALID_ARG). The workspace holds redmoe_balance_workspace_bytes(T, E) bytes;
+ * its control block is not used. T == 0
  * writes zeros forward and nothing backward. This library's own; the pages describe
  * inference only. */
 size_t redmoe_balance_workspace_bytes(int32_t T, int32_t E);

@@ -456,7 +456,7 @@ def _arg(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: i
     """The address of a tensor argument, checked; None stays None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on cuda:{dev}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
@@ -541,12 +541,13 @@ def redmoe_norm_forward(norm: Norm, h: torch.Tensor, h_out: Optional[torch.Tenso
                         x: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                         gate: Optional[torch.Tensor] = None, stream=None) -> None:
     """x <- N(h) (no y), or h_out [T,H] (may be h) and, where given, x [T,H] <- the residual step on (h, y)."""
-    dev, T = norm._dev(h, "h"), h.shape[0]
-    rows = (T, norm.hidden)
-    _call(load().redmoe_norm_forward, "redmoe_norm_forward", dev, stream, norm.ref, _arg(h, "h", rows, norm.h_torch, dev),
-          _arg(y, "y", rows, norm.y_torch, dev),
+    dev, T = norm._dev(h, "h"), h.size(0)
+    rows, ht = (T, norm.hidden), norm.h_torch
+    _call((_lib or load()).redmoe_norm_forward, "redmoe_norm_forward", dev, stream, norm.ref, _arg(h, "h", rows, ht, dev),
+          None if y is None else _arg(y, "y", rows, norm.y_torch, dev),
           None if gate is None else _arg(gate, "gate", norm.gate_shape(T), norm.gate_torch, dev), T,
-          _arg(h_out, "h_out", rows, norm.h_torch, dev), _arg(x, "x", rows, norm.x_torch, dev))
+          None if h_out is None else _arg(h_out, "h_out", rows, ht, dev),
+          None if x is None else _arg(x, "x", rows, norm.x_torch, dev))
 
 
 def redmoe_norm_workspace_bytes(norm: Norm, T: int) -> int:
@@ -579,7 +580,7 @@ def redmoe_norm_backward(norm: Norm, h_out: torch.Tensor, dh: torch.Tensor, work
     if dgate is not None:
         dg = _arg(dgate, "dgate", norm.gate_shape(T), norm.gate_torch if norm.gate == "element" else f32, dev)
     ws, nbytes = _work(workspace, dev)
-    _call(load().redmoe_norm_backward, "redmoe_norm_backward", dev, stream, norm.ref,
+    _call((_lib or load()).redmoe_norm_backward, "redmoe_norm_backward", dev, stream, norm.ref,
           _arg(h_out, "h_out", rows, norm.h_torch, dev), _arg(y, "y", rows, norm.y_torch, dev), g,
           _arg(dh_out, "dh_out", rows, norm.h_torch, dev), _arg(dx, "dx", rows, norm.x_torch, dev), T,
           _arg(dh, "dh", rows, norm.h_torch, dev), _arg(dy, "dy", rows, norm.y_torch, dev), dg,
@@ -608,7 +609,7 @@ def redmoe_forward_block(layer: Layer, before: Norm, after: Norm, h: torch.Tenso
     after._dev(h, "h")
     rows, picks = (T, layer.hidden), (T, layer.top_k)
     ws, nbytes = _work(workspace, dev)
-    _call(load().redmoe_forward_block, "redmoe_forward_block", dev, stream, layer.ref, before.ref, after.ref,
+    _call((_lib or load()).redmoe_forward_block, "redmoe_forward_block", dev, stream, layer.ref, before.ref, after.ref,
           _arg(h, "h", rows, before.h_torch, dev),
           None if gate is None else _arg(gate, "gate", after.gate_shape(T), after.gate_torch, dev), T,
           _arg(h_out, "h_out", rows, after.h_torch, dev), _arg(x_next, "x_next", rows, after.x_torch, dev),
@@ -654,7 +655,7 @@ def redmoe_balance_forward(logits: torch.Tensor, topk_ids: torch.Tensor, loss: t
     k = topk_ids.shape[1]
     f32, i32 = torch.float32, torch.int32
     ws, nbytes = _work(workspace, dev)
-    _call(load().redmoe_balance_forward, "redmoe_balance_forward", dev, stream, logits.data_ptr(), code,
+    _call((_lib or load()).redmoe_balance_forward, "redmoe_balance_forward", dev, stream, logits.data_ptr(), code,
           _arg(topk_ids, "topk_ids", (T, k), i32, dev), _mask(mask, T, dev), T, E, k, _arg(loss, "loss", (2,), f32, dev),
           _arg(counts, "counts", (E,), i32, dev), _arg(prob, "prob", (E,), f32, dev),
           _arg(n_rows, "n_rows", (1,), i32, dev), ws, nbytes)
@@ -666,7 +667,7 @@ def redmoe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, n_rows: 
     """dlogits [T,E] (the logits' dtype; may be logits) <- grad_loss[2] fp32, with the forward call's
     counts, n_rows and mask."""
     dev, code, T, E = _logits(logits)
-    _call(load().redmoe_balance_backward, "redmoe_balance_backward", dev, stream, logits.data_ptr(), code,
+    _call((_lib or load()).redmoe_balance_backward, "redmoe_balance_backward", dev, stream, logits.data_ptr(), code,
           _mask(mask, T, dev), T, E, top_k, _arg(counts, "counts", (E,), torch.int32, dev),
           _arg(n_rows, "n_rows", (1,), torch.int32, dev), _arg(grad_loss, "grad_loss", (2,), torch.float32, dev),
           _arg(dlogits, "dlogits", (T, E), logits.dtype, dev))
@@ -693,5 +694,5 @@ def redmoe_gemv(matrix: Matrix, x: torch.Tensor, y: torch.Tensor, stream=None) -
     T = x.shape[0]
     if x.dtype not in _CODES or y.dtype not in _CODES:
         raise ValueError(f"x and y are float32 or bfloat16: got {x.dtype} and {y.dtype}")
-    _call(load().redmoe_gemv, "redmoe_gemv", dev, stream, matrix.ref, _arg(x, "x", (T, matrix.cols), x.dtype, dev),
+    _call((_lib or load()).redmoe_gemv, "redmoe_gemv", dev, stream, matrix.ref, _arg(x, "x", (T, matrix.cols), x.dtype, dev),
           _CODES[x.dtype], T, _arg(y, "y", (T, matrix.rows), y.dtype, dev), _CODES[y.dtype])

@@ -25,6 +25,7 @@
 // not depend on timing.
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "vec8.cuh"
 
 namespace redmoe {
@@ -637,9 +638,7 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     int smem = p.ring_bytes * BAL_WARPS;
     const int sums = 4 * BAL_WARPS * E;
     smem = smem > sums ? smem : sums;
-    if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return REDMOE_ERR_CUDA;
+    if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     kern<<<blocks, 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
     if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -680,9 +679,7 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     p.depth = ring_depth(di.max_smem_optin / (E <= 512 ? 2 : 1) - 2 * 1024, E, logits_dtype, &p.ring_bytes);
     const int smem = p.ring_bytes * BAL_WARPS;
     const BackwardKernel kern = pick_backward(logits_dtype, E);
-    if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return REDMOE_ERR_CUDA;
+    if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     kern<<<balance_blocks(T, rows_a_block(E), 2 * di.sm_count), 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }

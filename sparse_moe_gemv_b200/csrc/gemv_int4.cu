@@ -37,6 +37,7 @@
 // waits for another until the end, and the loads in flight need no registers.
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
 
 #include <cuda_bf16.h>
 
@@ -489,8 +490,7 @@ bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
     const int fixed = P::fixed_bytes(p.T, p.K), room = (di.max_smem_optin - fixed) / P::WARP_BYTES;
     const int warps = room < P::WARPS ? room : P::WARPS, smem = fixed + warps * P::WARP_BYTES;
     const auto kern = gemv_kernel<NT, F32, WHOLE>;
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return false;
+    if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return false;
     const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles < di.sm_count ? tiles : di.sm_count);

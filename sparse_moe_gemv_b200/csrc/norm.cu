@@ -24,6 +24,7 @@
 // order.
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "norm.h"
 #include "vec8.cuh"
 
@@ -49,6 +50,8 @@ struct NormParams {
     float* part;  // backward: [blocks][2][H] column sums: dpre_w and A
     int units, ahead;  // walked rows: 16-byte units of a chunk, rows in flight (0 .. 2)
     bool want_pre, want_post, want_gate;
+    float *dpre_w, *dpost_w;
+    unsigned* ticket;   // backward: blocks that are done, where the last one adds the column sums; else NULL
 };
 
 // Sums of N values over the group: warps by shuffles, then the warps' sums through shared
@@ -300,6 +303,18 @@ __device__ __forceinline__ void shared_vectors(const NormParams& p, bool branch,
     }
 }
 
+// dpost_w and a channel gate's gradient in column c from that column's A (see below).
+__device__ __forceinline__ void finish_post(const NormParams& p, int c, float a) {
+    float v = p.block_scale;  // block_scale act(gate)
+    if (p.gate_kind == GATE_CHANNEL) {
+        const float g = load1(p.gate, p.gate_f32, c), w = p.post_w ? p.w_offset + load1(p.post_w, p.w_f32, c) : 1.0f;
+        const float act = p.sigmoid ? sigmoid(g) : g, dact = p.sigmoid ? act * (1.0f - act) : 1.0f;
+        if (p.want_gate) static_cast<float*>(p.dgate)[c] = a * (p.block_scale * dact) * w;
+        v *= act;
+    }
+    if (p.want_post) p.dpost_w[c] = p.gate_kind == GATE_TOKEN || p.gate_kind == GATE_ELEMENT ? a : a * v;
+}
+
 // Backward. The sums that a row needs are six, all of what is read:
 //   S = {h^2, dx pre h, y^2, dh_out e, dx pre e, h e},  e = y post (times an element gate)
 // since sum G e = S3 + r2 (S4 - k2 S5) with k2 = r2^2 S1 / H: one reduction a row, where summing G e
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
         }
     }
     if (!p.part) return;
-    asm volatile("griddepcontrol.launch_dependents;");  // norm_columns_kernel may take its place to wait
+    if (!p.ticket) asm volatile("griddepcontrol.launch_dependents;");  // norm_columns_kernel may take its place to wait
     // the groups' column sums, added in group order by group 0
     __syncthreads();
     if (group > 0) {
@@ -463,34 +478,56 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
         }
     }
     __syncthreads();
-    if (group > 0) return;
-    float* out = p.part + size_t(blockIdx.x) * 2 * p.H;
+    if (group == 0) {
+        float* out = p.part + size_t(blockIdx.x) * 2 * p.H;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = lane + i * p.tpr;
-        if (c >= p.chunks) continue;
-        for (int g = 0; g + 1 < rows; ++g) {
-            const uint32_t m = post + 4 * (g * 2 * p.H + 8 * c);
-            const F8 u = lds8f(m), v = lds8f(m + 4 * p.H);
+        for (int i = 0; i < NC; ++i) {
+            const int c = lane + i * p.tpr;
+            if (c >= p.chunks) continue;
+            for (int g = 0; g + 1 < rows; ++g) {
+                const uint32_t m = post + 4 * (g * 2 * p.H + 8 * c);
+                const F8 u = lds8f(m), v = lds8f(m + 4 * p.H);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc_pre[i].v[j] = __fadd2_rn(acc_pre[i].v[j], u.v[j]);
-                acc_post[i].v[j] = __fadd2_rn(acc_post[i].v[j], v.v[j]);
+                for (int j = 0; j < 4; ++j) {
+                    acc_pre[i].v[j] = __fadd2_rn(acc_pre[i].v[j], u.v[j]);
+                    acc_post[i].v[j] = __fadd2_rn(acc_post[i].v[j], v.v[j]);
+                }
             }
+            if (p.want_pre) store8<DT_F32>(out, c, acc_pre[i]);
+            if (p.want_post || p.want_gate) store8<DT_F32>(out + p.H, c, acc_post[i]);
         }
-        if (p.want_pre) store8<DT_F32>(out, c, acc_pre[i]);
-        if (p.want_post || p.want_gate) store8<DT_F32>(out + p.H, c, acc_post[i]);
+    }
+    if (!p.ticket) return;
+    // few partial rows: the block that is last to finish adds them, in block order
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+        if (last) *p.ticket = 0;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll 4
+        for (unsigned i = 0; i < gridDim.x; ++i) {
+            if (p.want_pre) a += __ldcg(p.part + size_t(i) * 2 * p.H + c);
+            if (p.want_post || p.want_gate) b += __ldcg(p.part + size_t(i) * 2 * p.H + p.H + c);
+        }
+        if (p.want_pre) p.dpre_w[c] = a;
+        finish_post(p, c, b);
     }
 }
 
 // dpre_w[col] = sum over blocks of part[block][0][col]; A[col] likewise from part[block][1] gives
 // dpost_w and a channel gate's gradient. 32 slices of the blocks, each in block order, then the
 // slices in order; a thread has four columns.
-__global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, int blocks, float* dpre, float* dpost,
-                                                           float* dgate) {
+__global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, int blocks) {
     __shared__ float4 sums[32][8];
     const int which = blockIdx.y, q = threadIdx.x & 7, slice = threadIdx.x >> 3;
-    if (which == 0 ? !dpre : !(dpost || dgate)) return;
+    if (which == 0 ? !p.want_pre : !(p.want_post || p.want_gate)) return;
     const int col = blockIdx.x * 32 + 4 * q;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -509,19 +546,8 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, i
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) a += reinterpret_cast<const float*>(&sums[i][threadIdx.x >> 2])[threadIdx.x & 3];
-    if (which == 0) {
-        dpre[c] = a;
-        return;
-    }
-    float v = p.block_scale, dv = p.block_scale;  // block_scale act(gate) and block_scale act'(gate)
-    if (p.gate_kind == GATE_CHANNEL) {
-        const float g = load1(p.gate, p.gate_f32, c), w = p.post_w ? p.w_offset + load1(p.post_w, p.w_f32, c) : 1.0f;
-        const float act = p.sigmoid ? sigmoid(g) : g;
-        dv *= p.sigmoid ? act * (1.0f - act) : 1.0f;
-        v *= act;
-        if (dgate) dgate[c] = a * dv * w;
-    }
-    if (dpost) dpost[c] = p.gate_kind == GATE_TOKEN || p.gate_kind == GATE_ELEMENT ? a : a * v;
+    if (which == 0) p.dpre_w[c] = a;
+    else finish_post(p, c, a);
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -544,6 +570,7 @@ NormShape norm_shape(int H, long long T, int sm_count) {
 // An upper bound on the blocks of the backward pass that needs no device: the workspace query
 // works without one.
 constexpr int MAX_SMS = 160, MAX_BLOCKS_SM = 2;
+constexpr int TICKET_WORD = 8;  // of the workspace's control block
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -644,10 +671,6 @@ int rows_smem(NormParams& p, const NormShape& s, int want, int max_smem) {
     const int smem = fixed + (p.ahead + 1) * stage, ends = (s.rows - 1) * 2 * p.H * 4;
     return smem > ends ? smem : ends;
 }
-bool set_smem(NormKernel kern, int smem) {
-    return smem <= 40 * 1024 || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
-}
-
 }  // namespace
 
 redmoe_status norm_forward_check(const redmoe_norm* N, const void* h, const void* y, const void* gate, int T,
@@ -773,6 +796,8 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     p.dy = dy;
     p.dgate = dgate;
     p.part = work ? reinterpret_cast<float*>(static_cast<char*>(workspace) + 256) : nullptr;
+    p.dpre_w = dpre_w;
+    p.dpost_w = dpost_w;
     p.want_pre = dpre_w != nullptr;
     p.want_post = dpost_w != nullptr;
     p.want_gate = dgate != nullptr && channel;
@@ -783,10 +808,15 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
               (branch && N->gate_kind == GATE_ELEMENT ? units(N->gate_dtype) : 0);
     const int smem = rows_smem(p, s, want, di.max_smem_optin);
     const NormKernel kern = pick_backward(N, s.nc, threads, branch);
-    if (!set_smem(kern, smem)) return REDMOE_ERR_CUDA;
+    if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
+    // Up to so many partial sums the last block adds them itself. That saves the host a launch (13.0
+    // -> 10.7 us a call of 37 rows of 264 from Python) and costs the GPU 2 us behind a fence and a
+    // counter (5.0 -> 7.2 us); with 16 rows of 2048 it would cost 12.
+    const bool one = work && (long long)blocks * p.H <= 4096;
+    p.ticket = one ? static_cast<unsigned*>(workspace) + TICKET_WORD : nullptr;
     kern<<<blocks, threads, smem, stm>>>(p);
     if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
-    if (!work) return REDMOE_OK;
+    if (!work || one) return REDMOE_OK;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.H + 31) / 32, 2);
     cfg.blockDim = dim3(256);
@@ -796,9 +826,7 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_columns_kernel, p, blocks, dpre_w, dpost_w,
-                                             p.want_gate ? static_cast<float*>(dgate) : static_cast<float*>(nullptr));
-    return e == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, norm_columns_kernel, p, blocks) == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 }  // extern "C"

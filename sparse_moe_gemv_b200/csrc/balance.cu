@@ -96,9 +96,17 @@ struct Ring {
     uint32_t base;
     int in, use;            // bytes from base
     unsigned lives;         // whether the lane's row counts, in the groups asked for: newest in bit 0
-    bool live;              // in the next one
+    unsigned bits, bits2;   // whether the lane's row counts in the LPR groups from the next on, and in those behind
+    int pos, row2;          // place in `bits`; the row that this lane looks up next
 
-    __device__ __forceinline__ bool counts(int t) const { return t < T && (!mask || __ldg(mask + t)); }
+    // The mask bytes of LPR groups, a lane each: one load for as many rows of the lane's own.
+    __device__ __forceinline__ unsigned look() {
+        bool m = row2 < T;
+        if (m && mask) m = __ldg(mask + row2);
+        row2 += LPR * step;
+        const unsigned all = __ballot_sync(FULL, m);
+        return LPR == 32 ? all : (all >> ((threadIdx.x & 31) / LPR * LPR)) & ((1u << (LPR & 31)) - 1u);
+    }
     __device__ __forceinline__ void start(const void* logits, const uint8_t* m, int T_, int E, int depth_, unsigned char* b,
                                           int t0, int step_) {
         const int lane = threadIdx.x & 31;
@@ -112,12 +120,16 @@ struct Ring {
         step_bytes = size_t(step) * (size_t(E) * SIZE);
         in = use = 0;
         lives = 0;
-        live = counts(row);
+        row2 = row + lane % LPR * step;
+        pos = 0;
+        bits = look();
+        bits2 = look();
         for (int i = 0; i + 1 < depth; ++i) ask();
     }
-    // One group of copies (nothing of rows that do not count); the mask bytes of the one behind it.
+    // One group of copies (nothing of rows that do not count).
     __device__ __forceinline__ void ask() {
         const int lane = threadIdx.x & 31, l = lane % LPR;
+        const bool live = (bits >> pos) & 1u;
         const uint32_t dst = base + in + 16 * lane;
         if constexpr (FLAT) {
             if (__any_sync(FULL, live)) {
@@ -140,7 +152,11 @@ struct Ring {
         lives = (lives << 1) | (live ? 1u : 0u);
         src += step_bytes;
         row += step;
-        live = counts(row);
+        if (++pos == LPR) {
+            pos = 0;
+            bits = bits2;
+            bits2 = look();
+        }
     }
     // Ask for one more group and wait for the oldest: its values, -infinity beyond the columns and in
     // rows that do not count. Returns whether any of the warp's rows does.
@@ -246,7 +262,7 @@ __global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_f
     __shared__ double zsum[WARPS];
     __shared__ int nsum[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
-    // T is at most 2^30, and rows are asked for at most six steps (a step: 2^15 rows) beyond it
+    // T is at most 2^30, and row numbers go at most 100 steps of up to 20,480 rows beyond it
     const int step = gridDim.x * WARPS * RPW;
     int t0 = (blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;  // the warp's first row, and this lane's
     Ring<DT, VEC, NCH, LPR> ring;

@@ -18,10 +18,12 @@
 //   dy      = r1 (c - y r1^2 mean(c y))
 //
 // Both are bound by memory: forward reads y and h once and writes h_out and x once, backward
-// reads h_out, y, dh_out and dx once and writes dh and dy once. A row lies in the registers of
-// a group of threads (whole warps, eight columns a thread), so the statistics cost one
-// reduction over the group each and nothing is read twice. All sums are fp32, in a fixed
-// order.
+// reads h_out, y, dh_out and dx once and writes dh and dy once. A row belongs to a group of
+// threads (whole warps, eight or sixteen columns a thread) that holds it on chip, so the
+// statistics cost reductions over the group and nothing is read twice. All sums are fp32, in a
+// fixed order. Measured on a B200, of the copy bandwidth: forward 8191 x 5120 fp32 with an element
+// gate 106 us (84%), 8192 x 4096 47 us (86%), 2048 x 2048 12.1 us (53%: under two waves of blocks),
+// one row of 2048 1.8 us; backward 8192 x 2048 48 us (63%: some sixty instructions an element).
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -54,59 +56,20 @@ struct NormParams {
     unsigned* ticket;   // backward: blocks that are done, where the last one adds the column sums; else NULL
 };
 
-// Sums of N values over the group: warps by shuffles, then the warps' sums through shared
-// memory in warp order. `buf` alternates between two areas from call to call, so that one
-// barrier a call is enough: an area is written again only behind the barrier of the call
-// between, which every thread reaches after its reads.
-constexpr int RED = 3 * 16;  // floats of an area: up to three sums of up to 16 warps a group
-
-// Warp sums of two or three values, two lanes' worth at a time: the halves of the warp exchange and
-// keep different values, so the later steps carry fewer. Afterwards lane 0 has v[0], lane 8 v[1] and
-// lane 16 v[2] (N = 3), or lane 0 v[0] and lane 16 v[1] (N = 2); returns this lane's.
-template <int N>
-__device__ __forceinline__ float warp_sums(const float (&v)[N]) {
-    const bool high = threadIdx.x & 16, mid = threadIdx.x & 8;
-    float a;
-    if constexpr (N == 1) {
-        a = v[0] + __shfl_xor_sync(FULL, v[0], 16);
-        a += __shfl_xor_sync(FULL, a, 8);
-    } else if constexpr (N == 2) {
-        a = (high ? v[1] : v[0]) + __shfl_xor_sync(FULL, high ? v[0] : v[1], 16);
-        a += __shfl_xor_sync(FULL, a, 8);
-    } else {
-        a = (high ? v[2] : v[0]) + __shfl_xor_sync(FULL, high ? v[0] : v[2], 16);
-        const float b = v[1] + __shfl_xor_sync(FULL, v[1], 16);
-        // lower half: keep v[0] or v[1] by the bit of 8; upper half: v[2] in both
-        const float keep = !high && mid ? b : a, give = !high && !mid ? b : a;
-        a = keep + __shfl_xor_sync(FULL, give, 8);
-    }
-    a += __shfl_xor_sync(FULL, a, 4);
-    a += __shfl_xor_sync(FULL, a, 2);
-    return a + __shfl_xor_sync(FULL, a, 1);
-}
-
-template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int tpr, int group, int wig) {
-    const float a = warp_sums<N>(v);
-    const int l = threadIdx.x & 31;
-    const int which = N == 1 ? (l == 0 ? 0 : -1) : N == 2 ? (l == 0 ? 0 : l == 16 ? 1 : -1)
-                                                          : (l == 0 ? 0 : l == 8 ? 1 : l == 16 ? 2 : -1);
-    if (tpr == 32) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(FULL, a, N == 3 ? 8 * i : 16 * i);
-        return;
-    }
-    if (which >= 0) buf[which * 16 + wig] = a;
+// The sum over a group: warps by shuffles, then the warps' sums through shared memory in warp
+// order. Successive sums take their `buf` ([16], zeros behind the group's last warp) from two areas
+// in turn, so one barrier a sum is enough: an area is written again only behind the barrier of the
+// sum between, which every thread reaches after its reads.
+constexpr int RED = 16;
+__device__ __forceinline__ float group_sum(float v, float* buf, int tpr, int group, int wig) {
+    v = warp_sum(v);
+    if (tpr == 32) return v;
+    if ((threadIdx.x & 31) == 0) buf[wig] = v;
     asm volatile("bar.sync %0, %1;" :: "r"(group + 1), "r"(tpr) : "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    for (int w = 0; w < tpr / 32; w += 4) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float4 f = *reinterpret_cast<const float4*>(buf + i * 16 + w);  // zeros behind the last warp
-            v[i] += (f.x + f.y) + (f.z + f.w);
-        }
-    }
+    const float4 f = *reinterpret_cast<const float4*>(buf + ((threadIdx.x & 3) << 2));
+    v = (f.x + f.y) + (f.z + f.w);
+    v += __shfl_xor_sync(FULL, v, 1);
+    return v + __shfl_xor_sync(FULL, v, 2);
 }
 
 // Six sums over the group at once: eight lanes' worth of values is halved three times while the warp
@@ -202,9 +165,7 @@ __global__ void __launch_bounds__(512, 2) norm_forward_kernel(const NormParams p
             float2 q = both(0.0f);
 #pragma unroll
             for (int i = 0; i < NC; ++i) dot(y[i], y[i], q);
-            float s[1] = {q.x + q.y};
-            group_sum<1>(s, red[0][group], p.tpr, group, wig);
-            scale *= rsqrtf(fmaf(s[0], p.inv_h, p.eps));
+            scale *= rsqrtf(fmaf(group_sum(q.x + q.y, red[0][group], p.tpr, group, wig), p.inv_h, p.eps));
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -230,9 +191,7 @@ __global__ void __launch_bounds__(512, 2) norm_forward_kernel(const NormParams p
     float2 q = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) dot(h[i], h[i], q);  // zero beyond the row
-    float s[1] = {q.x + q.y};
-    group_sum<1>(s, red[1][group], p.tpr, group, wig);
-    const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps));
+    const float r2 = rsqrtf(fmaf(group_sum(q.x + q.y, red[1][group], p.tpr, group, wig), p.inv_h, p.eps));
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = lane + i * p.tpr;
@@ -327,7 +286,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
     constexpr int AT_G = UH, AT_X = 2 * UH, AT_Y = AT_X + UX, AT_GATE = AT_Y + UY;  // units: h_out, dh_out, dx, y, gate
     extern __shared__ __align__(16) float dyn[];  // post, pre [H] each, then the rows' units; at the end
                                                   // the column sums [groups - 1][2][H]
-    __shared__ __align__(16) float red[2][8][RED6];
+    constexpr int GROUPS = THREADS == 512 ? 1 : NORM_THREADS / 32;  // over 256 threads are one row's
+    __shared__ __align__(16) float red[2][GROUPS][RED6];
     const int group = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr, wig = lane / 32;
     const int rows = blockDim.x / p.tpr;
     clear_unused(red[0][group], red[1][group], RED6, lane, p.tpr);
@@ -664,13 +624,15 @@ int units(int dt) { return dt == DT_F32 ? 2 : 1; }
 // Shared memory of a kernel that walks rows, and with it p.ahead: two rows in flight where `want`
 // blocks of an SM can hold them, else one, else none.
 int rows_smem(NormParams& p, const NormShape& s, int want, int max_smem) {
-    const int stage = s.nc * p.units * s.tpr * s.rows * 16, fixed = 2 * p.H * 4, own = 2 * 8 * RED6 * 4;
-    const int room = max_smem / want - own - (want > 1 ? 1024 : 0);  // 1 KiB of every block is the system's
+    const int stage = s.nc * p.units * s.tpr * s.rows * 16, fixed = 2 * p.H * 4;
+    const int own = 2 * (s.tpr * s.rows > 256 ? 1 : 8) * RED6 * 4 + 64;  // static
+    const int room = max_smem / want - own - (want > 1 ? 1024 : 0);      // 1 KiB of every block is the system's
     p.ahead = 2;
     while (p.ahead > 0 && fixed + (p.ahead + 1) * stage > room) --p.ahead;
     const int smem = fixed + (p.ahead + 1) * stage, ends = (s.rows - 1) * 2 * p.H * 4;
     return smem > ends ? smem : ends;
 }
+
 }  // namespace
 
 redmoe_status norm_forward_check(const redmoe_norm* N, const void* h, const void* y, const void* gate, int T,

@@ -186,7 +186,7 @@ template <int NT> struct Plan {
     static constexpr int WROW = COLS / 2 + 16;      // bytes of a slot's row of W (bank offset)
     static constexpr int SROW = COLS / 16;          // bytes of a slot's row of scales
     static constexpr int NA = M * 4 * (ONE ? 1 : NT);              // sums a lane holds
-    static constexpr int SLOTS = NT == 2 ? 3 : 2;                  // of a warp's ring
+    static constexpr int SLOTS = 2;                                // of a warp's ring
     static constexpr int SLOT = ROWS * (WROW + SROW);
     static constexpr int WARP_BYTES = SLOTS * SLOT + NA * 32 * 4;  // shared memory of a warp
     static constexpr int fixed_bytes(int T, int K) {               // and of a block besides

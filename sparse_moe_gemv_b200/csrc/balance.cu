@@ -253,7 +253,8 @@ struct BalanceParams {
 };
 
 template <int DT, int VEC, int NCH, int LPR, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_forward_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(32 * WARPS, LPR == 32 && NCH * VEC <= 16 ? 2 : 1)
+    balance_forward_kernel(const BalanceParams p) {
     constexpr int N2 = NCH * VEC / 2, THREADS = 32 * WARPS, RPW = 32 / LPR;  // pairs of a lane, rows of a warp
     // the warps' rings; behind the last row cols [WARPS][E], whose first row becomes the block's sums
     extern __shared__ __align__(16) float sm[];
@@ -487,7 +488,7 @@ __device__ __forceinline__ void store_logits(void* out, size_t row, int E, int l
 }
 
 template <int DT, int VEC, int NCH, int LPR, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, NCH * VEC <= 16 ? 2 : 1) balance_backward_kernel(const BalanceGradParams p) {
+__global__ void __launch_bounds__(32 * WARPS, 1) balance_backward_kernel(const BalanceGradParams p) {
     constexpr int N2 = NCH * VEC / 2, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
     const int step = gridDim.x * WARPS * RPW;
@@ -569,10 +570,10 @@ int ring_depth(int room, int E, int dtype, int* bytes) {
     return depth;
 }
 
-// 16-byte chunks where every row starts on one, else single values; eight lanes a row up to 128
-// columns; the smallest number of chunks a lane needs.
 int rows_a_block(int E) { return E <= 128 ? 4 * BAL_WARPS : BAL_WARPS; }
 
+// 16-byte chunks where every row starts on one, else single values; eight lanes a row up to 128
+// columns; the smallest number of chunks a lane needs.
 #define BALANCE_PICK(kernel)                                                                              \
     do {                                                                                                  \
         constexpr int F = DT_F32, B = DT_BF16, W = BAL_WARPS;                                             \
@@ -632,7 +633,7 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     DevInfo di;
     if (!get_dev_info(&di)) return REDMOE_ERR_CUDA;
     // two blocks an SM (one above 512 columns)
-    const int each = E <= 512 ? 2 : 1, most = each * di.sm_count;
+    const int each = E > 128 && E <= 512 ? 2 : 1, most = each * di.sm_count;
     const int blocks = balance_blocks(T, rows_a_block(E), most < BAL_MAX_BLOCKS ? most : BAL_MAX_BLOCKS);
     const BalanceWs w = balance_layout(blocks, E);
     char* base = static_cast<char*>(workspace);
@@ -692,11 +693,11 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     p.n_rows = n_rows;
     p.grad = grad_loss;
     p.dlogits = dlogits;
-    p.depth = ring_depth(di.max_smem_optin / (E <= 512 ? 2 : 1) - 2 * 1024, E, logits_dtype, &p.ring_bytes);
+    p.depth = ring_depth(di.max_smem_optin - 2 * 1024, E, logits_dtype, &p.ring_bytes);
     const int smem = p.ring_bytes * BAL_WARPS;
     const BackwardKernel kern = pick_backward(logits_dtype, E);
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
-    kern<<<balance_blocks(T, rows_a_block(E), 2 * di.sm_count), 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    kern<<<balance_blocks(T, rows_a_block(E), di.sm_count), 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 

@@ -314,7 +314,8 @@ redmoe_status redmoe_forward_noalloc(const redmoe_layer *L, const void *x, int32
  *
  * g is 1 (REDMOE_GATE_NONE), or act(gate) with gate [T] (TOKEN), [hidden] (CHANNEL) or
  * [T, hidden] (ELEMENT), act the identity (LINEAR) or the logistic function (SIGMOID).
- * Statistics are fp32; x is computed from h_out before h_out is rounded to h_dtype, so
+ * Statistics are fp32 (a row whose sum of squares passes the fp32 range is normalised to zero
+ * where it is finite); x is computed from h_out before h_out is rounded to h_dtype, so
  * every output is rounded once. Rows are independent; T = 1 and long batches run the same
  * kernel. hidden is a multiple of 8 up to 8192 (more: REDMOE_ERR_UNSUPPORTED); dtypes are
  * REDMOE_F32 or REDMOE_BF16; tensors are 16-byte aligned (a TOKEN gate: to its element).
@@ -407,8 +408,7 @@ redmoe_status redmoe_forward_block(const redmoe_layer *L, const redmoe_norm *bef
  * REDMOE_F32 or REDMOE_BF16, 16-byte aligned. Sums over rows have a fixed order: results do
  * not depend on timing. Outputs must not overlap inputs or one another
  * (REDMOE_ERR_INVALID_ARG). The workspace holds redmoe_balance_workspace_bytes(T, E) bytes;
- * its control block is not used. T == 0
- * writes zeros forward and nothing backward. This library's own; the pages describe
+ * its control block is not used. T == 0 writes zeros forward and nothing backward. This library's own; the pages describe
  * inference only. */
 size_t redmoe_balance_workspace_bytes(int32_t T, int32_t E);
 redmoe_status redmoe_balance_forward(const void *logits, int32_t logits_dtype, const int32_t *topk_ids,
@@ -424,8 +424,13 @@ redmoe_status redmoe_balance_backward(const void *logits, int32_t logits_dtype, 
  * projections beside the layer: y[t, n] = sum_k x[t, k] W[n, k], T = 0..32 token rows (more:
  * REDMOE_ERR_UNSUPPORTED). W is REDMOE_INT4G32 (others: REDMOE_ERR_UNSUPPORTED), x
  * REDMOE_BF16 [T, cols], y REDMOE_F32 or REDMOE_BF16 [T, rows], overwritten, aligned to its
- * element. cols is a multiple of 32 up to 65536. Products are exact and sums fp32; the order
- * of summation is fixed for given sizes. y must not overlap x or W. */
+ * element. cols is a multiple of 32 up to 65536. Products are exact (but for elements of x under
+ * 2^-116 of their row's largest), sums are fp32 in an order that is fixed for given sizes; their
+ * rounding is in proportion to 16 times the sum of |scale x|, since they run over the stored
+ * nibbles 0 .. 15. A row of x that holds an infinity or a NaN makes its row of y NaN; other rows
+ * are not affected. W is read once for all rows of x if they fit on a multiprocessor (at T = 8
+ * up to 8192 columns, at 16 up to 4608, at 32 up to 2304), else once for every share of them that
+ * does. y must not overlap x or W. */
 typedef struct redmoe_matrix {
     int32_t rows;            /* N                                                             */
     int32_t cols;            /* K                                                             */

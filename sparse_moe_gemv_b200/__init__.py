@@ -462,6 +462,13 @@ def _arg(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: i
     return t.data_ptr()
 
 
+def _int32(n: int, name: str) -> int:
+    """A size that the library takes as int32 (ctypes would cut a longer one silently)."""
+    if not -2**31 <= n < 2**31:
+        raise ValueError(f"{name} = {n} is beyond int32")
+    return n
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -512,7 +519,7 @@ class Norm:
                 raise ValueError(f"norm weights are float32 or bfloat16: got {first.dtype}")
             self.device = _device_of(first, "pre_w" if pre_w is not None else "post_w")
         s = _Norm()
-        s.hidden = hidden
+        s.hidden = _int32(hidden, "hidden")
         s.h_dtype, s.y_dtype, s.x_dtype = DTYPES[h_dtype], DTYPES[y_dtype], DTYPES[x_dtype]
         s.w_dtype = _CODES[first.dtype] if first is not None else 0
         s.post_norm = int(post_w is not None if post_norm is None else post_norm)
@@ -541,7 +548,7 @@ def redmoe_norm_forward(norm: Norm, h: torch.Tensor, h_out: Optional[torch.Tenso
                         x: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                         gate: Optional[torch.Tensor] = None, stream=None) -> None:
     """x <- N(h) (no y), or h_out [T,H] (may be h) and, where given, x [T,H] <- the residual step on (h, y)."""
-    dev, T = norm._dev(h, "h"), h.size(0)
+    dev, T = norm._dev(h, "h"), _int32(h.size(0), "T")
     rows, ht = (T, norm.hidden), norm.h_torch
     _call((_lib or load()).redmoe_norm_forward, "redmoe_norm_forward", dev, stream, norm.ref, _arg(h, "h", rows, ht, dev),
           None if y is None else _arg(y, "y", rows, norm.y_torch, dev),
@@ -551,7 +558,7 @@ def redmoe_norm_forward(norm: Norm, h: torch.Tensor, h_out: Optional[torch.Tenso
 
 
 def redmoe_norm_workspace_bytes(norm: Norm, T: int) -> int:
-    return int(load().redmoe_norm_workspace_bytes(norm.ref, int(T)))
+    return int(load().redmoe_norm_workspace_bytes(norm.ref, _int32(int(T), "T")))
 
 
 def new_norm_workspace(norm: Norm, T: int, device=None) -> torch.Tensor:
@@ -572,7 +579,7 @@ def redmoe_norm_backward(norm: Norm, h_out: torch.Tensor, dh: torch.Tensor, work
                          stream=None) -> None:
     """dh, dy, dgate, dpost_w and dpre_w (fp32 [H]) <- the gradients dh_out and dx that arrive at
     h_out and x. dgate is fp32 for a token or channel gate, the gate's dtype for an element gate."""
-    dev, T = norm._dev(h_out, "h_out"), h_out.shape[0]
+    dev, T = norm._dev(h_out, "h_out"), _int32(h_out.size(0), "T")
     rows, cols, f32 = (T, norm.hidden), (norm.hidden,), torch.float32
     g = dg = None
     if gate is not None:
@@ -588,7 +595,7 @@ def redmoe_norm_backward(norm: Norm, h_out: torch.Tensor, dh: torch.Tensor, work
 
 
 def redmoe_workspace_bytes_block(layer: Layer, T: int) -> int:
-    return int(load().redmoe_workspace_bytes_block(layer.ref, int(T)))
+    return int(load().redmoe_workspace_bytes_block(layer.ref, _int32(int(T), "T")))
 
 
 def new_workspace_block(layer: Layer, T: int, device=None) -> torch.Tensor:
@@ -605,8 +612,11 @@ def redmoe_forward_block(layer: Layer, before: Norm, after: Norm, h: torch.Tenso
                          stream=None) -> None:
     """The residual block around the layer: x = N(h) by `before`, y = layer(x), then `after`'s step on
     (h, y) into h_out (may be h) and, where given, x_next."""
-    dev, T = before._dev(h, "h"), h.shape[0]
+    dev, T = before._dev(h, "h"), _int32(h.size(0), "T")
     after._dev(h, "h")
+    for name, t in layer.tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"the layer's {name} is on {t.device}, h on cuda:{dev}")
     rows, picks = (T, layer.hidden), (T, layer.top_k)
     ws, nbytes = _work(workspace, dev)
     _call((_lib or load()).redmoe_forward_block, "redmoe_forward_block", dev, stream, layer.ref, before.ref, after.ref,
@@ -618,7 +628,7 @@ def redmoe_forward_block(layer: Layer, before: Norm, after: Norm, h: torch.Tenso
 
 
 def redmoe_balance_workspace_bytes(T: int, n_experts: int) -> int:
-    return int(load().redmoe_balance_workspace_bytes(int(T), int(n_experts)))
+    return int(load().redmoe_balance_workspace_bytes(_int32(int(T), "T"), _int32(int(n_experts), "n_experts")))
 
 
 def new_balance_workspace(T: int, n_experts: int, device=None) -> torch.Tensor:
@@ -635,7 +645,7 @@ def _logits(logits: torch.Tensor):
     if code is None or logits.dim() != 2 or not logits.is_contiguous():
         raise ValueError(f"logits: expected a contiguous float32 or bfloat16 [T, E] tensor, got {logits.dtype} "
                          f"{list(logits.shape)}")
-    return dev, code, logits.shape[0], logits.shape[1]
+    return dev, code, _int32(logits.shape[0], "T"), _int32(logits.shape[1], "E")
 
 
 def _mask(mask: Optional[torch.Tensor], T: int, dev: int):
@@ -652,7 +662,7 @@ def redmoe_balance_forward(logits: torch.Tensor, topk_ids: torch.Tensor, loss: t
     dev, code, T, E = _logits(logits)
     if topk_ids.dim() != 2:
         raise ValueError(f"topk_ids: expected [T, k], got {list(topk_ids.shape)}")
-    k = topk_ids.shape[1]
+    k = _int32(topk_ids.shape[1], "k")
     f32, i32 = torch.float32, torch.int32
     ws, nbytes = _work(workspace, dev)
     _call((_lib or load()).redmoe_balance_forward, "redmoe_balance_forward", dev, stream, logits.data_ptr(), code,
@@ -668,7 +678,7 @@ def redmoe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, n_rows: 
     counts, n_rows and mask."""
     dev, code, T, E = _logits(logits)
     _call((_lib or load()).redmoe_balance_backward, "redmoe_balance_backward", dev, stream, logits.data_ptr(), code,
-          _mask(mask, T, dev), T, E, top_k, _arg(counts, "counts", (E,), torch.int32, dev),
+          _mask(mask, T, dev), T, E, _int32(top_k, "top_k"), _arg(counts, "counts", (E,), torch.int32, dev),
           _arg(n_rows, "n_rows", (1,), torch.int32, dev), _arg(grad_loss, "grad_loss", (2,), torch.float32, dev),
           _arg(dlogits, "dlogits", (T, E), logits.dtype, dev))
 
@@ -682,6 +692,7 @@ class Matrix:
             dev = _device_of(w, "w")
             _arg(w, "w", (rows, cols // 2), torch.uint8, dev)
             _arg(s, "s", (rows, cols // 32), torch.bfloat16, dev)
+        _int32(rows, "rows"), _int32(cols, "cols")
         st = _Matrix()
         st.rows, st.cols, st.dtype, st.w, st.s = rows, cols, DTYPES[dtype], _ptr(w), _ptr(s)
         self.struct, self.ref = st, C.byref(st)
@@ -691,7 +702,7 @@ class Matrix:
 def redmoe_gemv(matrix: Matrix, x: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """y[T, rows] (fp32 or bf16) <- x[T, cols] bf16 times the matrix's transpose, T = 0..32."""
     dev = _device_of(matrix.w, "w")
-    T = x.shape[0]
+    T = _int32(x.size(0), "T")
     if x.dtype not in _CODES or y.dtype not in _CODES:
         raise ValueError(f"x and y are float32 or bfloat16: got {x.dtype} and {y.dtype}")
     _call((_lib or load()).redmoe_gemv, "redmoe_gemv", dev, stream, matrix.ref, _arg(x, "x", (T, matrix.cols), x.dtype, dev),

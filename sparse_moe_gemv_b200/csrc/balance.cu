@@ -21,8 +21,10 @@
 // and 16-bit rows need several in flight for full bandwidth). Forward, every block leaves its sums in
 // the workspace and a second kernel, one cluster that waits where the first one ends, adds them: the
 // last block of the first kernel doing that took 6 to 10 us behind fences and a counter, this takes
-// 3. Sums over rows are made in a fixed order (lane, warp, block), counts are integers: results do
-// not depend on timing.
+// 3. Measured on a B200: forward 65536 x 512 fp32 32 us (65% of the copy bandwidth, the exponentials and
+// sums of 33 million values beside the launch of two kernels), 2048 x 512 9.8 us; backward 32768 x 512
+// fp32 25 us (82%). Sums over rows are made in a fixed order (lane, warp, block), counts are integers:
+// results do not depend on timing.
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -573,7 +575,8 @@ int ring_depth(int room, int E, int dtype, int* bytes) {
 int rows_a_block(int E) { return E <= 128 ? 4 * BAL_WARPS : BAL_WARPS; }
 
 // 16-byte chunks where every row starts on one, else single values; eight lanes a row up to 128
-// columns; the smallest number of chunks a lane needs.
+// columns (65536 rows of 64 fp32 14.1 us, of 61 17.5; a whole warp a row 19.2 and 34.1); the smallest
+// number of chunks a lane needs.
 #define BALANCE_PICK(kernel)                                                                              \
     do {                                                                                                  \
         constexpr int F = DT_F32, B = DT_BF16, W = BAL_WARPS;                                             \
@@ -632,7 +635,8 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     }
     DevInfo di;
     if (!get_dev_info(&di)) return REDMOE_ERR_CUDA;
-    // two blocks an SM (one above 512 columns)
+    // Two blocks an SM where a warp has one row at a time (65536 rows of 512: 32.3 us, one block 33.6)
+    // and registers allow, one with deeper rings for short rows (65536 rows of 61: 16.0 us, two 17.5).
     const int each = E > 128 && E <= 512 ? 2 : 1, most = each * di.sm_count;
     const int blocks = balance_blocks(T, rows_a_block(E), most < BAL_MAX_BLOCKS ? most : BAL_MAX_BLOCKS);
     const BalanceWs w = balance_layout(blocks, E);
@@ -656,18 +660,9 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     const int sums = 4 * BAL_WARPS * E;
     smem = smem > sums ? smem : sums;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
-    kern<<<blocks, 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return REDMOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(BAL_CLUSTER);
-    cfg.blockDim = dim3(FIN_THREADS);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, balance_finish_kernel, p) == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, false, p)) return REDMOE_ERR_CUDA;
+    return launch(balance_finish_kernel, dim3(BAL_CLUSTER), FIN_THREADS, 0, s, true, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, const uint8_t* row_mask, int32_t T,
@@ -693,12 +688,15 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     p.n_rows = n_rows;
     p.grad = grad_loss;
     p.dlogits = dlogits;
+    // one block an SM with the deepest ring: 32768 rows of 512 25.0 us (82% of the copy bandwidth; two
+    // blocks 25.4), in bf16 and a fifth of them masked 16.5 (18.3)
     p.depth = ring_depth(di.max_smem_optin - 2 * 1024, E, logits_dtype, &p.ring_bytes);
     const int smem = p.ring_bytes * BAL_WARPS;
     const BackwardKernel kern = pick_backward(logits_dtype, E);
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
-    kern<<<balance_blocks(T, rows_a_block(E), di.sm_count), 32 * BAL_WARPS, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? REDMOE_OK : REDMOE_ERR_CUDA;
+    const int blocks = balance_blocks(T, rows_a_block(E), di.sm_count);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, false, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -35,6 +35,10 @@
 // shared memory in warp order, so results do not depend on timing. Each warp copies its steps
 // into a ring of its own with asynchronous copies (128-byte lines asked for whole), so no warp
 // waits for another until the end, and the loads in flight need no registers.
+//
+// Measured on a B200: 151936 x 2048 at one token 34.2 us (26.7 at the copy bandwidth; the steady rate
+// is 93% of it, five to six us are the launch, x and the last steps). 24571 x 4096 at 13 tokens 24.4
+// us (8.6): bound by the reads of x from shared memory, which every 16 rows of W repeat.
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -175,7 +179,15 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
     __syncthreads();
 }
 
-// What a pass over NT blocks of eight tokens, or (NT = 0) over one token, uses.
+// What a pass over NT blocks of eight tokens, or (NT = 0) over one token, uses. Two tokens already
+// take the block of eight: 18.5 us where a kernel for two like the one for one took 20.6 (24571 x
+// 4096). Each number against its neighbours, in us:
+//   M      two tiles a step up to eight tokens: 15.9, 16.4, 19.5 (T = 2, 4, 8; 24571 x 4096), one
+//          tile 16.7, 17.4, 18.5; with more blocks of eight there are no registers for a second
+//   WARPS  20 and 16: 34.2 (T = 1, 151936 x 2048) and 16.4 (T = 4); 12 warps 37.8 and 18.0
+//   COLS   512 at one token 35.1 (151936 x 2048), 256 37.5
+//   SLOTS  2: 34.2, 16.4, 24.4, 26.3 (T = 1, 4, 13; T = 32 at 24571 x 2048), 3: 36.8, 17.7, 26.5,
+//          30.2: what a third slot asks for first costs more than the second leaves open
 template <int NT> struct Plan {
     static constexpr bool ONE = NT == 0;
     static constexpr int TOK = ONE ? 1 : 8 * NT;    // tokens that sums are kept for
@@ -492,17 +504,7 @@ bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
     const auto kern = gemv_kernel<NT, F32, WHOLE>;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return false;
     const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles < di.sm_count ? tiles : di.sm_count);
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
+    return launch(kern, dim3(tiles < di.sm_count ? tiles : di.sm_count), 32 * warps, smem, stream, true, p);
 }
 
 // Whether T tokens of K columns leave room for eight warps' rings.

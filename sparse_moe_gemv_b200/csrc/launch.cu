@@ -3,8 +3,6 @@
 
 #include <mutex>
 
-#include <cuda_runtime.h>
-
 namespace redmoe {
 namespace {
 
@@ -28,7 +26,10 @@ bool allow_smem(const void* kern, int bytes) {
     for (int i = 0; i < n_allowed && !at; ++i)
         if (allowed[i].kern == kern && allowed[i].dev == dev) at = &allowed[i];
     if (at && at->bytes >= bytes) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
     if (at) at->bytes = bytes;
     else if (n_allowed < MAX_ALLOWED) allowed[n_allowed++] = {kern, dev, bytes};
     return true;

@@ -1,10 +1,32 @@
-// Launch helpers of the operators around the layer.
+// Launch helpers of the operators around the layer. A failure is the call's own: nothing is left in
+// the runtime's last-error state for a later call to find, and none is taken from there.
 #pragma once
+
+#include <cuda_runtime.h>
 
 namespace redmoe {
 
 // Allow `kern` (a __global__ function) `bytes` of dynamic shared memory on the current device. What
 // has been allowed is remembered, so a call that asks again costs a lookup; false on a CUDA error.
 bool allow_smem(const void* kern, int bytes);
+
+// kern(args...). `early`: the blocks may be placed while the kernel before on the stream ends; the
+// kernel waits for that end itself (griddepcontrol.wait).
+template <class... P, class... A>
+bool launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, bool early, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
 
 }  // namespace redmoe

@@ -1,8 +1,9 @@
 """Per-expert counts, balance and z loss and their gradient (redmoe_balance_*) against the
 definition in 64 bits.
 
-Tolerances: counts and rows are exact. A probability is a few units off (expf, one reciprocal, a
-sum of at most 32 values of a lane and 5 shuffles): under 64 U; its mean adds the rows of a warp,
+Tolerances: counts and rows are exact. A probability is a few units off (the exponent
+v - max rounded: |v - max| units, at most 20 for logits of two standard deviations; ex2 and one
+reciprocal; a sum of at most 32 values of a lane and 5 shuffles): under 64 U; its mean adds the rows of a warp,
 16 warps and the blocks, each one U: T / 16 + 64 + 160 more. The gradient is one such row.
 """
 

@@ -130,6 +130,37 @@ def test_no_rows_streams_and_graph(gpu_lib):
     check(w, s, x, y)
 
 
+@pytest.mark.parametrize("T", [1, 5, 13, 32])
+def test_calls_that_feed_one_another(gpu_lib, T):
+    """A call's kernel may be placed while the one before it ends: a chain of products, each reading what
+    the one before wrote and writing what the one before read, equals the same calls one at a time."""
+    mats = [smg.Matrix(*make(512, 512, 1, seed=i)[:2], 512, 512) for i in range(6)]
+    x = make(512, 512, T, seed=9)[2] * 0.05
+    buf = [x.clone(), torch.empty_like(x)]
+    want = x
+    for i in range(60):
+        y = torch.empty_like(x)
+        smg.redmoe_gemv(mats[i % 6], want, y)
+        torch.cuda.synchronize()
+        want = (y.float() * 2.0 ** -5).to(torch.bfloat16)  # about what 512 products grow by: exact
+    scaled = [smg.Matrix(m.w, m.s * 2.0 ** -5, 512, 512) for m in mats]
+
+    def chain():
+        for i in range(60):
+            smg.redmoe_gemv(scaled[i % 6], buf[i % 2], buf[1 - i % 2])
+
+    chain()
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and float(want.abs().max()) > 0 and torch.equal(buf[0], want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    buf[0].copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(buf[0], want)
+
+
 def test_offsets_beyond_32_bits(gpu_lib):
     """More than 2^31 bytes of packed weights."""
     N, K = 140001, 32768

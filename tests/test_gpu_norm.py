@@ -2,9 +2,10 @@
 in 64 bits.
 
 Tolerances: every result is a fixed expression of fp32 operations on exact inputs. A sum over a
-row is at most 16 products of a thread, 5 shuffle steps and 16 warps deep, rsqrtf, expf and the
-divide add a few units, and each of the few further products one: under 64 U of the result's
-magnitude forward. Backward chains two such reductions, and a column sum adds the rows of a
+row is at most 16 products of a thread, 5 shuffle steps and 16 warps deep, rsqrtf adds a few units,
+each of the few further products one, and the logistic function of a gate a up to |a| + 6 (the exponent's
+rounding, ex2 and the reciprocal), a dozen for normal gates: under 64 U of the result's magnitude
+forward. Backward chains two such reductions, and a column sum adds the rows of a
 thread, up to 8 groups and up to 37 + 8 blocks: under 256 U for the sizes here. A stored value
 adds half a step of its type.
 """
@@ -222,6 +223,58 @@ def test_same_bits_twice_on_another_stream_and_in_a_graph(gpu_lib):
     want, want_x = forward(norm, t)
     grads = backward(norm, t, T, H)
     assert torch.equal(ho, want) and torch.equal(x, want_x) and all(torch.equal(o[n], grads[n]) for n in grads)
+
+
+@pytest.mark.parametrize("T,H", [(5, 264), (37, 64), (300, 16), (64, 2048)])
+def test_repeated_calls_with_one_workspace(gpu_lib, T, H):
+    """Few sums are added by the last block, more by a second kernel: both leave the control block zero
+    and the same workspace serves the next call, other sizes, gradients left out and replays included."""
+    norm, t, kw = make(T, H, post=True, kind="channel")
+    first = backward(norm, t, T, H)
+    ws = smg.new_norm_workspace(norm, T)
+    o = {n: torch.empty_like(v) for n, v in first.items()}
+
+    def call(rows=T, **drop):
+        kw = dict(dgate=o["dgate"], dpost_w=o["dpost_w"], dpre_w=o["dpre_w"])
+        kw.update(drop)
+        smg.redmoe_norm_backward(norm, t["h"][:rows], o["dh"][:rows], ws, dh_out=t["dh_out"][:rows], dx=t["dx"][:rows],
+                                 y=t["y"][:rows], gate=t["gate"], dy=o["dy"][:rows], **kw)
+
+    for drop in ({}, dict(dgate=None), dict(dpost_w=None), dict(dpre_w=None), dict(rows=1), dict(dgate=None, dpre_w=None)):
+        call(**drop)
+        torch.cuda.synchronize()
+        assert int(ws[:256].count_nonzero()) == 0
+        for v in o.values():
+            v.fill_(float("nan"))
+        call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o[n], first[n]) for n in first) and int(ws[:256].count_nonzero()) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        call()
+    for _ in range(3):
+        for v in o.values():
+            v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o[n], first[n]) for n in first) and int(ws[:256].count_nonzero()) == 0
+
+
+def test_calls_at_once_with_workspaces_of_their_own(gpu_lib):
+    cases = [make(T, H, post=True, kind="channel", seed=i) for i, (T, H) in enumerate([(37, 64), (700, 512), (5, 264), (64, 2048)])]
+    want = [backward(n, t, *t["h"].shape) for n, t, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    works = [smg.new_norm_workspace(n, t["h"].shape[0]) for n, t, _ in cases]
+    got = [{k: torch.empty_like(v) for k, v in w.items()} for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (n, t, _), o, ws, s in zip(cases, got, works, streams):
+            smg.redmoe_norm_backward(n, t["h"], o["dh"], ws, dh_out=t["dh_out"], dx=t["dx"], y=t["y"], gate=t["gate"],
+                                     dy=o["dy"], dgate=o["dgate"], dpost_w=o["dpost_w"], dpre_w=o["dpre_w"], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(o[k], w[k]) for k in w)
 
 
 def test_offsets_beyond_32_bits(gpu_lib):

@@ -132,6 +132,7 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
                                         float* gsum, int* exps, uint32_t* tops) {
     const int runs = (stride - GV_PAD) / 16, steps = runs / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    constexpr int BATCH = ONE ? 1 : 4;  // one token: hardly a run or a group for every warp
     for (int t = sh.first; t < p.T; t += sh.step) {  // the runs this thread asked for
         uint32_t m = 0;
 #pragma unroll 4
@@ -149,30 +150,41 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
         // e is -126 (also for rows of subnormals) .. 128 (infinity or NaN); the scale as two factors
         const int e = max(int(top >> 7), 1) - 127, up = GV_TOP - e, f0 = up / 2, f1 = up - f0;
         const uint32_t a = pow2_pair(f0), b = pow2_pair(f1), c = pow2_pair(f1 - 4);
-#pragma unroll 4
-        for (int r = 32 * sh.part + lane; r < runs; r += 32 * sh.parts) {
-            uint4* at = reinterpret_cast<uint4*>(xs + t * stride + 16 * r);
-            const uint4 v = *at;
-            *at = make_uint4(mul2(mul2(__byte_perm(v.x, v.z, 0x5410), a), b), mul2(mul2(__byte_perm(v.x, v.z, 0x7632), a), c),
-                             mul2(mul2(__byte_perm(v.y, v.w, 0x5410), a), b), mul2(mul2(__byte_perm(v.y, v.w, 0x7632), a), c));
+        uint4* row = reinterpret_cast<uint4*>(xs + t * stride);
+        for (int r0 = 32 * sh.part + lane; r0 < runs; r0 += 32 * BATCH * sh.parts) {
+            uint4 in[BATCH];  // several at a time: in place, a load would wait for the store before it
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (r0 + 32 * i * sh.parts < runs) in[i] = row[r0 + 32 * i * sh.parts];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const uint4 v = in[i];
+                if (r0 + 32 * i * sh.parts < runs)
+                    row[r0 + 32 * i * sh.parts] =
+                        make_uint4(mul2(mul2(__byte_perm(v.x, v.z, 0x5410), a), b), mul2(mul2(__byte_perm(v.x, v.z, 0x7632), a), c),
+                                   mul2(mul2(__byte_perm(v.y, v.w, 0x5410), a), b), mul2(mul2(__byte_perm(v.y, v.w, 0x7632), a), c));
+            }
         }
         if (lane == 0 && sh.part == 0) exps[t] = e;
     }
     __syncthreads();
     constexpr int NB = ONE ? 1 : TOK / 8;  // blocks of eight tokens
     const int g = lane >> 2, q = lane & 3;
-#pragma unroll 4
-    for (int i = warp; i < 8 * steps * NB; i += warps) {
-        const int group = i / NB, t0 = 8 * (i - group * NB);
-        const uint4 x = *reinterpret_cast<const uint4*>((t0 + g < p.T ? xs + (t0 + g) * stride + 64 * group : zero) + 16 * q);
-        float d[4];
-        mma_word(d, 0x88888888u, 0x88888888u, x, 0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = warp; i < 8 / BATCH * steps * NB; i += warps) {  // groups of a block of eight tokens
+        const int first = BATCH * (i / NB), t0 = 8 * (i % NB);
+        const unsigned char* from = (t0 + g < p.T ? xs + (t0 + g) * stride + 64 * first : zero) + 16 * q;
+        const int next = t0 + g < p.T ? 64 : 0;
+        uint4 x[BATCH];
+        float d[BATCH][4];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) x[j] = *reinterpret_cast<const uint4*>(from + j * next);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) mma_word(d[j], 0x88888888u, 0x88888888u, x[j], 0.0f, 0.0f, 0.0f, 0.0f);
         if (g == 0) {  // every row of the sums is the same; this lane has tokens t0 + 2 q and the next
-            const int t = t0 + 2 * q;
-            if (ONE) {
-                if (t == 0) gsum[group] = -d[0];
-            } else {
-                *reinterpret_cast<float2*>(gsum + group * TOK + t) = make_float2(-d[0], -d[1]);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                if (!ONE) *reinterpret_cast<float2*>(gsum + (first + j) * TOK + t0 + 2 * q) = make_float2(-d[j][0], -d[j][1]);
+                else if (q == 0) gsum[first + j] = -d[j][0];
             }
         }
     }

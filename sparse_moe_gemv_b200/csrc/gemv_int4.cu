@@ -194,16 +194,16 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
 // What a pass over NT blocks of eight tokens, or (NT = 0) over one token, uses. Two tokens already
 // take the block of eight: 18.5 us where a kernel for two like the one for one took 20.6 (24571 x
 // 4096). Each number against its neighbours, in us:
-//   M      two tiles a step up to eight tokens: 15.9, 16.4, 19.5 (T = 2, 4, 8; 24571 x 4096), one
-//          tile 16.7, 17.4, 18.5; with more blocks of eight there are no registers for a second
+//   M      two tiles a step up to eight tokens, see two_tiles; with more blocks of eight, steps of two
+//          tiles of 256 or 128 columns take 31.9 and 29.7, one tile 24.5 (T = 13, 24571 x 4096)
 //   WARPS  20 and 16: 34.2 (T = 1, 151936 x 2048) and 16.4 (T = 4); 12 warps 37.8 and 18.0
 //   COLS   512 at one token 35.1 (151936 x 2048), 256 37.5
 //   SLOTS  2: 34.2, 16.4, 24.4, 26.3 (T = 1, 4, 13; T = 32 at 24571 x 2048), 3: 36.8, 17.7, 26.5,
 //          30.2: what a third slot asks for first costs more than the second leaves open
-template <int NT> struct Plan {
+template <int NT, int M_ = 1> struct Plan {
     static constexpr bool ONE = NT == 0;
     static constexpr int TOK = ONE ? 1 : 8 * NT;    // tokens that sums are kept for
-    static constexpr int M = NT == 1 ? 2 : 1;       // tiles of 16 rows in a step: x is read once for them
+    static constexpr int M = M_;                    // tiles of 16 rows in a step: x is read once for them
     static constexpr int WARPS = ONE ? 20 : 16;                    // at most
     static constexpr int ROWS = 16 * M;
     static constexpr int COLS = ONE ? 512 : 256;    // columns of a step: one or two slices
@@ -360,10 +360,10 @@ __device__ __forceinline__ void put(void* y, size_t i, float v) {
 }
 
 // NT = 0: one token; otherwise NT blocks of eight. All of x in shared memory.
-template <int NT, bool F32, bool WHOLE>
-__global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const GemvParams p) {
+template <int NT, int M, bool F32, bool WHOLE>
+__global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(const GemvParams p) {
     extern __shared__ __align__(16) unsigned char sm[];
-    using P = Plan<NT>;
+    using P = Plan<NT, M>;
     constexpr bool ONE = P::ONE;
     constexpr int TOK = P::TOK, NA = P::NA, ROWS = P::ROWS, RING = P::SLOTS * P::SLOT;
     const int steps = (p.K + P::COLS - 1) / P::COLS, slices = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(32 * Plan<NT>::WARPS, 1) gemv_kernel(const Gem
                 const unsigned char* xp[NX];
 #pragma unroll
                 for (int i = 0; i < NX; ++i) xp[i] = x0[i] + s * xstep[i] + h * (xstep[i] / 2);
-                row_step<P, NT, P::M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * TOK, acc);
+                row_step<P, NT, M>(w + 64 * h, sc + 8 * h, [&]() { if (h == 1) release(); }, xp, my_g + (8 * s + 4 * h) * TOK, acc);
             }
         }
         slot = slot + P::SLOT == RING ? 0 : slot + P::SLOT;
@@ -508,18 +508,32 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 }
 
 // One pass over W for p.T tokens.
-template <int NT, bool F32, bool WHOLE>
+template <int NT, int M, bool F32, bool WHOLE>
 bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
-    using P = Plan<NT>;
+    using P = Plan<NT, M>;
     const int fixed = P::fixed_bytes(p.T, p.K), room = (di.max_smem_optin - fixed) / P::WARP_BYTES;
     const int warps = room < P::WARPS ? room : P::WARPS, smem = fixed + warps * P::WARP_BYTES;
-    const auto kern = gemv_kernel<NT, F32, WHOLE>;
+    const auto kern = gemv_kernel<NT, M, F32, WHOLE>;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return false;
     const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
     return launch(kern, dim3(tiles < di.sm_count ? tiles : di.sm_count), 32 * warps, smem, stream, true, p);
 }
 
-// Whether T tokens of K columns leave room for eight warps' rings.
+// Whether up to eight tokens take steps of two tiles: where all warps' rings fit beside x (24571 x
+// 4096: 16.1, 16.3, 16.8 us at T = 2, 4, 5, one tile 16.5, 17.3, 17.9; but 18.5, 18.3, 19.6 against
+// 18.1, 18.2, 18.3 at T = 6, 7, 8, which leave 15, 14, 13 warps), where blocks have more than one such
+// step's rows (4736 x 4096: 8.1 against 7.7 us at T = 4) and where the coarser shares give none a tenth
+// more rows (2048 x 4096, 32 instead of 16: 7.7 against 6.7 us at T = 4).
+bool two_tiles(const GemvParams& p, const DevInfo& di) {
+    using P = Plan<1, 2>;
+    if (P::fixed_bytes(p.T, p.K) + P::WARPS * P::WARP_BYTES > di.max_smem_optin) return false;
+    const int t1 = (p.N + 15) / 16, t2 = (p.N + 31) / 32, sms = di.sm_count;
+    return t2 > sms && 20 * ((t2 + sms - 1) / sms) <= 11 * ((t1 + sms - 1) / sms);
+}
+
+// Whether T tokens of K columns leave room for eight warps' rings. Eight warps are slower than sixteen
+// but faster than two passes (24571 x 5120 at T = 16: 39.1 us, as two passes of eight 41.9), six no
+// longer (x 5376: 48.6 and 44.1).
 bool fits(int T, int K, int smem) {
     const int need = T == 1    ? Plan<0>::fixed_bytes(T, K) + 8 * Plan<0>::WARP_BYTES
                      : T <= 8  ? Plan<1>::fixed_bytes(T, K) + 8 * Plan<1>::WARP_BYTES
@@ -530,10 +544,10 @@ bool fits(int T, int K, int smem) {
 
 template <bool F32, bool WHOLE>
 bool launch_tokens(const GemvParams& p, const DevInfo& di, cudaStream_t s) {
-    if (p.T == 1) return launch_gemv<0, F32, WHOLE>(p, di, s);
-    if (p.T <= 8) return launch_gemv<1, F32, WHOLE>(p, di, s);
-    if (p.T <= 16) return launch_gemv<2, F32, WHOLE>(p, di, s);
-    return launch_gemv<4, F32, WHOLE>(p, di, s);
+    if (p.T == 1) return launch_gemv<0, 1, F32, WHOLE>(p, di, s);
+    if (p.T <= 8) return two_tiles(p, di) ? launch_gemv<1, 2, F32, WHOLE>(p, di, s) : launch_gemv<1, 1, F32, WHOLE>(p, di, s);
+    if (p.T <= 16) return launch_gemv<2, 1, F32, WHOLE>(p, di, s);
+    return launch_gemv<4, 1, F32, WHOLE>(p, di, s);
 }
 
 }  // namespace
@@ -564,10 +578,9 @@ extern "C" redmoe_status redmoe_gemv(const redmoe_matrix* W, const void* x, int3
     p.s = static_cast<const uint16_t*>(W->s);
     p.N = W->rows;
     p.K = W->cols;
-    // Token rows at a time: all, or as many as leave room for eight rings, in whole blocks of eight
-    // if more than that. Each pass over W serves one such share.
+    // Token rows at a time: all, or an equal share of them that leaves room for eight rings.
     int most = T;
-    while (most > 1 && !fits(most, p.K, di.max_smem_optin)) most = most > 8 ? (most - 1) / 8 * 8 : most - 1;
+    for (int n = 2; most > 1 && !fits(most, p.K, di.max_smem_optin); ++n) most = (T + n - 1) / n;
     const bool f32 = y_dtype == DT_F32, whole = p.K % GV_COLS == 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int t = 0; t < T; t += most) {

@@ -21,8 +21,8 @@
 // and 16-bit rows need several in flight for full bandwidth). Forward, every block leaves its sums in
 // the workspace and a second kernel, one cluster that waits where the first one ends, adds them: the
 // last block of the first kernel doing that took 6 to 10 us behind fences and a counter, this takes
-// 3. Measured on a B200: forward 65536 x 512 fp32 32 us (65% of the copy bandwidth, the exponentials and
-// sums of 33 million values beside the launch of two kernels), 2048 x 512 9.8 us; backward 32768 x 512
+// 3. Measured on a B200: forward 65536 x 512 fp32 31.6 us (66% of the copy bandwidth, the exponentials and
+// sums of 33 million values beside the launch of two kernels), 2048 x 512 9.6 us; backward 32768 x 512
 // fp32 25 us (82%). Sums over rows are made in a fixed order (lane, warp, block), counts are integers:
 // results do not depend on timing.
 #include "common.cuh"
@@ -33,9 +33,10 @@
 namespace redmoe {
 namespace {
 
-constexpr int BAL_WARPS = 16;
+constexpr int BAL_WARPS = 16;           // of a block, where no more are named
+constexpr int BAL_WARPS_MID = 24;       // forward, rows of 129 .. 512 columns
 constexpr int BAL_CLUSTER = 8;         // blocks of the second kernel
-constexpr int BAL_MAX_BLOCKS = 2 * 160;  // of the first: two an SM
+constexpr int BAL_MAX_BLOCKS = 160;    // of the first: one an SM
 __host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }  // a row of sums in the workspace
 
 // A row lies over its LPR lanes in chunks of VEC consecutive values, chunk l + LPR i for lane l. VEC > 1
@@ -255,10 +256,10 @@ struct BalanceParams {
 };
 
 template <int DT, int VEC, int NCH, int LPR, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, LPR == 32 && NCH * VEC <= 16 ? 2 : 1)
-    balance_forward_kernel(const BalanceParams p) {
-    constexpr int N2 = NCH * VEC / 2, THREADS = 32 * WARPS, RPW = 32 / LPR;  // pairs of a lane, rows of a warp
-    // the warps' rings; behind the last row cols [WARPS][E], whose first row becomes the block's sums
+__global__ void __launch_bounds__(32 * WARPS, 1) balance_forward_kernel(const BalanceParams p) {
+    constexpr int N2 = NCH * VEC / 2, RPW = 32 / LPR;  // pairs of a lane, rows of a warp
+    const int threads = blockDim.x, warps = threads >> 5;  // up to WARPS
+    // the warps' rings; behind the last row cols [warps][E], whose first row becomes the block's sums
     extern __shared__ __align__(16) float sm[];
     float* cols = sm;
     __shared__ int hist[MAX_EXPERTS];
@@ -266,11 +267,11 @@ __global__ void __launch_bounds__(32 * WARPS, LPR == 32 && NCH * VEC <= 16 ? 2 :
     __shared__ int nsum[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR;
     // T is at most 2^30, and row numbers go at most 100 steps of up to 20,480 rows beyond it
-    const int step = gridDim.x * WARPS * RPW;
-    int t0 = (blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;  // the warp's first row, and this lane's
+    const int step = gridDim.x * warps * RPW;
+    int t0 = (blockIdx.x * warps + warp) * RPW, t = t0 + lane / LPR;  // the warp's first row, and this lane's
     Ring<DT, VEC, NCH, LPR> ring;
     ring.start(p.logits, p.mask, p.T, p.E, p.depth, reinterpret_cast<unsigned char*>(sm) + warp * p.ring_bytes, t0, step);
-    for (int e = threadIdx.x; e < p.E; e += THREADS) hist[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += threads) hist[e] = 0;
     const int32_t* ids = p.ids + size_t(t) * p.k + l;
     const size_t ids_step = size_t(step) * p.k;
     int id_next = t < p.T && l < p.k ? __ldg(ids) : -1;
@@ -332,16 +333,16 @@ __global__ void __launch_bounds__(32 * WARPS, LPR == 32 && NCH * VEC <= 16 ? 2 :
         nsum[warp] = rows;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    for (int e = threadIdx.x; e < p.E; e += threads) {
         float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += cols[w * p.E + e];
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) s += cols[w * p.E + e];
         p.ws_prob[size_t(blockIdx.x) * padded(p.E) + e] = s;
         p.ws_counts[size_t(blockIdx.x) * padded(p.E) + e] = hist[e];
     }
     if (warp == 0) {
-        double z = lane < WARPS ? zsum[lane] : 0.0;
-        int n = lane < WARPS ? nsum[lane] : 0;
+        double z = lane < warps ? zsum[lane] : 0.0;
+        int n = lane < warps ? nsum[lane] : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             z += __shfl_xor_sync(FULL, z, o);
@@ -556,7 +557,7 @@ int balance_blocks(int T, int rows, int most) {
 }
 
 // Depth of the rings in `room` bytes of shared memory (2, 3, 4 or 6 slots), and a ring's bytes.
-int ring_depth(int room, int E, int dtype, int* bytes) {
+int ring_depth(int room, int warps, int E, int dtype, int* bytes) {
     const int size = dtype == DT_F32 ? 4 : 2, rows = E <= 128 ? 4 : 1;
     // rows of whole chunks: the lanes' places, at most 16 columns (E <= 128) or E / 32 rounded up to a
     // power of two each
@@ -566,37 +567,44 @@ int ring_depth(int room, int E, int dtype, int* bytes) {
                                            : (E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 8 : E <= 512 ? 16 : 32);
         slot = 32 * values * size;
     }
-    const int fits = room / BAL_WARPS / slot;
+    const int fits = room / warps / slot;
     const int depth = fits >= 6 ? 6 : (fits >= 4 ? 4 : (fits == 3 ? 3 : 2));
     *bytes = depth * slot;
     return depth;
 }
 
-int rows_a_block(int E) { return E <= 128 ? 4 * BAL_WARPS : BAL_WARPS; }
+int rows_a_block(int E, int warps) { return E <= 128 ? 4 * warps : warps; }
+
+// Warps of a block of the forward pass. Rows of 129 .. 512 columns take 24: 31.5 us for 65536 rows of 512
+// (two blocks of 16 an SM 32.4), in bf16 27.8 (30.7), of 501 37.8 (48.1: 64 registers are too few); but
+// 16 while that leaves a row to each (2048 rows: 9.5 us, 10.1 in fewer blocks).
+int forward_warps(int T, int E, int sm_count) {
+    return E > 128 && E <= 512 && T > BAL_WARPS * sm_count ? BAL_WARPS_MID : BAL_WARPS;
+}
 
 // 16-byte chunks where every row starts on one, else single values; eight lanes a row up to 128
 // columns (65536 rows of 64 fp32 14.1 us, of 61 17.5; a whole warp a row 19.2 and 34.1); the smallest
 // number of chunks a lane needs.
-#define BALANCE_PICK(kernel)                                                                              \
+#define BALANCE_PICK(kernel, V)                                                                             \
     do {                                                                                                  \
         constexpr int F = DT_F32, B = DT_BF16, W = BAL_WARPS;                                             \
         if (dtype == B && E % 8 == 0)                                                                     \
-            return E <= 64 ? kernel<B, 8, 1, 8, W> : E <= 128 ? kernel<B, 8, 2, 8, W> : E <= 256 ? kernel<B, 8, 1, 32, W> \
-                 : E <= 512 ? kernel<B, 8, 2, 32, W> : kernel<B, 8, 4, 32, W>;                            \
+            return E <= 64 ? kernel<B, 8, 1, 8, W> : E <= 128 ? kernel<B, 8, 2, 8, W> : E <= 256 ? kernel<B, 8, 1, 32, V> \
+                 : E <= 512 ? kernel<B, 8, 2, 32, V> : kernel<B, 8, 4, 32, W>;                            \
         if (dtype == F && E % 4 == 0)                                                                     \
-            return E <= 32 ? kernel<F, 4, 1, 8, W> : E <= 128 ? kernel<F, 4, 4, 8, W> : E <= 256 ? kernel<F, 4, 2, 32, W> \
-                 : E <= 512 ? kernel<F, 4, 4, 32, W> : kernel<F, 4, 8, 32, W>;                            \
+            return E <= 32 ? kernel<F, 4, 1, 8, W> : E <= 128 ? kernel<F, 4, 4, 8, W> : E <= 256 ? kernel<F, 4, 2, 32, V> \
+                 : E <= 512 ? kernel<F, 4, 4, 32, V> : kernel<F, 4, 8, 32, W>;                            \
         if (dtype == F)                                                                                   \
-            return E <= 32 ? kernel<F, 1, 4, 8, W> : E <= 128 ? kernel<F, 1, 16, 8, W> : E <= 512 ? kernel<F, 1, 16, 32, W> \
+            return E <= 32 ? kernel<F, 1, 4, 8, W> : E <= 128 ? kernel<F, 1, 16, 8, W> : E <= 512 ? kernel<F, 1, 16, 32, V> \
                  : kernel<F, 1, 32, 32, W>;                                                               \
-        return E <= 32 ? kernel<B, 1, 4, 8, W> : E <= 128 ? kernel<B, 1, 16, 8, W> : E <= 512 ? kernel<B, 1, 16, 32, W> \
+        return E <= 32 ? kernel<B, 1, 4, 8, W> : E <= 128 ? kernel<B, 1, 16, 8, W> : E <= 512 ? kernel<B, 1, 16, 32, V> \
              : kernel<B, 1, 32, 32, W>;                                                                   \
     } while (0)
 
 using ForwardKernel = void (*)(BalanceParams);
 using BackwardKernel = void (*)(BalanceGradParams);
-ForwardKernel pick_forward(int dtype, int E) { BALANCE_PICK(balance_forward_kernel); }
-BackwardKernel pick_backward(int dtype, int E) { BALANCE_PICK(balance_backward_kernel); }
+ForwardKernel pick_forward(int dtype, int E) { BALANCE_PICK(balance_forward_kernel, BAL_WARPS_MID); }
+BackwardKernel pick_backward(int dtype, int E) { BALANCE_PICK(balance_backward_kernel, BAL_WARPS); }
 #undef BALANCE_PICK
 
 }  // namespace
@@ -608,7 +616,7 @@ extern "C" {
 
 size_t redmoe_balance_workspace_bytes(int32_t T, int32_t E) {
     if (T < 0 || E <= 0 || E > MAX_EXPERTS) return 0;
-    return balance_layout(balance_blocks(T, rows_a_block(E), BAL_MAX_BLOCKS), E).total;
+    return balance_layout(balance_blocks(T, rows_a_block(E, BAL_WARPS), BAL_MAX_BLOCKS), E).total;
 }
 
 redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, const int32_t* topk_ids,
@@ -635,10 +643,8 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     }
     DevInfo di;
     if (!get_dev_info(&di)) return REDMOE_ERR_CUDA;
-    // Two blocks an SM where a warp has one row at a time (65536 rows of 512: 32.3 us, one block 33.6)
-    // and registers allow, one with deeper rings for short rows (65536 rows of 61: 16.0 us, two 17.5).
-    const int each = E > 128 && E <= 512 ? 2 : 1, most = each * di.sm_count;
-    const int blocks = balance_blocks(T, rows_a_block(E), most < BAL_MAX_BLOCKS ? most : BAL_MAX_BLOCKS);
+    const int warps = forward_warps(T, E, di.sm_count), most = di.sm_count < BAL_MAX_BLOCKS ? di.sm_count : BAL_MAX_BLOCKS;
+    const int blocks = balance_blocks(T, rows_a_block(E, warps), most);
     const BalanceWs w = balance_layout(blocks, E);
     char* base = static_cast<char*>(workspace);
     BalanceParams p;
@@ -655,13 +661,13 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     p.ws_counts = reinterpret_cast<int32_t*>(base + w.counts);
     p.ws_tail = reinterpret_cast<Tail*>(base + w.tail);
     const ForwardKernel kern = pick_forward(logits_dtype, E);
-    p.depth = ring_depth(di.max_smem_optin / each - 8 * 1024, E, logits_dtype, &p.ring_bytes);  // less the static part
-    int smem = p.ring_bytes * BAL_WARPS;
-    const int sums = 4 * BAL_WARPS * E;
+    p.depth = ring_depth(di.max_smem_optin - 8 * 1024, warps, E, logits_dtype, &p.ring_bytes);  // less the static part
+    int smem = p.ring_bytes * warps;
+    const int sums = 4 * warps * E;
     smem = smem > sums ? smem : sums;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, false, p)) return REDMOE_ERR_CUDA;
+    if (!launch(kern, dim3(blocks), 32 * warps, smem, s, false, p)) return REDMOE_ERR_CUDA;
     return launch(balance_finish_kernel, dim3(BAL_CLUSTER), FIN_THREADS, 0, s, true, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
@@ -690,11 +696,11 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     p.dlogits = dlogits;
     // one block an SM with the deepest ring: 32768 rows of 512 25.0 us (82% of the copy bandwidth; two
     // blocks 25.4), in bf16 and a fifth of them masked 16.5 (18.3)
-    p.depth = ring_depth(di.max_smem_optin - 2 * 1024, E, logits_dtype, &p.ring_bytes);
+    p.depth = ring_depth(di.max_smem_optin - 2 * 1024, BAL_WARPS, E, logits_dtype, &p.ring_bytes);
     const int smem = p.ring_bytes * BAL_WARPS;
     const BackwardKernel kern = pick_backward(logits_dtype, E);
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
-    const int blocks = balance_blocks(T, rows_a_block(E), di.sm_count);
+    const int blocks = balance_blocks(T, rows_a_block(E, BAL_WARPS), di.sm_count);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, false, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }

@@ -34,6 +34,9 @@ namespace redmoe {
 namespace {
 
 constexpr int NORM_MAX_H = 8192;
+// An upper bound on the blocks of the backward pass that needs no device: the workspace query
+// works without one.
+constexpr int MAX_SMS = 160, MAX_BLOCKS_SM = 2;
 constexpr int NORM_THREADS = 256;  // threads of a block whose groups are smaller than that
 
 enum : int { GATE_NONE = 0, GATE_TOKEN = 1, GATE_CHANNEL = 2, GATE_ELEMENT = 3 };
@@ -227,6 +230,16 @@ __device__ __forceinline__ F8 lds8(uint32_t at, int stride) {  // one chunk of U
     else return bf16x8(a);
 }
 __device__ __forceinline__ F8 lds8f(uint32_t at) { return f32x8(lds16(at), lds16(at + 16)); }
+// The shared vectors lie as the chunks' first four values, then their last four: lanes at 16-byte steps
+// use every bank once, where 32-byte steps would use every second one twice.
+__device__ __forceinline__ void put_shared(float* to, int chunks, int c, const F8& v) {
+    float4* p = reinterpret_cast<float4*>(to);
+    p[c] = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
+    p[chunks + c] = make_float4(v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y);
+}
+__device__ __forceinline__ F8 get_shared(uint32_t from, int chunks, int c) {
+    return f32x8(lds16(from + 16 * c), lds16(from + 16 * (chunks + c)));
+}
 
 template <int U>
 __device__ __forceinline__ void copy_units(uint32_t dst, int stride, const void* p, size_t chunk) {
@@ -253,14 +266,14 @@ __device__ __forceinline__ void shared_vectors(const NormParams& p, bool branch,
         if (p.post_w) b.load(p.post_w, p.w_f32, c);
         const bool channel = branch && p.gate_kind == GATE_CHANNEL;
         if (channel) g.load(p.gate, p.gate_f32, c);
-        store8<DT_F32>(pre, c, p.pre_w ? add(a.get(p.w_f32), p.w_offset) : fill8(1.0f));
+        put_shared(pre, p.chunks, c, p.pre_w ? add(a.get(p.w_f32), p.w_offset) : fill8(1.0f));
         F8 v = p.post_w ? add(b.get(p.w_f32), p.w_offset) : fill8(1.0f);
         if (channel) {
             const F8 w = g.get(p.gate_f32);
             v = mul(v, p.sigmoid ? sigmoid(w) : w);
         }
         if (channel || (branch && p.gate_kind == GATE_NONE)) v = mul(v, p.block_scale);
-        store8<DT_F32>(post, c, v);
+        put_shared(post, p.chunks, c, v);
     }
 }
 
@@ -370,13 +383,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
                 read(at + i * chunk_bytes);
                 F8 e;
                 if constexpr (BRANCH) {
-                    e = mul(y, lds8f(post + 32 * c));
+                    e = mul(y, get_shared(post, p.chunks, c));
                     if (element) e = mul(e, v);
                     dot(y, y, q[2]);
                     dot(dho, e, q[3]);
                 }
                 if (has_x) {
-                    const F8 ap = mul(a, lds8f(pre + 32 * c));
+                    const F8 ap = mul(a, get_shared(pre, p.chunks, c));
                     dot(h, h, q[0]);
                     dot(ap, h, q[1]);
                     if constexpr (BRANCH) {
@@ -404,13 +417,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
             F8 G = dho;
             if (has_x) {
                 acc_pre[i] = fma(a, mul(h, r2), acc_pre[i]);
-                G = fma(fma(h, -k2, mul(a, lds8f(pre + 32 * c))), r2, G);
+                G = fma(fma(h, -k2, mul(a, get_shared(pre, p.chunks, c))), r2, G);
             }
             if constexpr (!BRANCH) {
                 store8<HD>(p.dh, row + c, G);
             } else {
                 store8<HD>(p.dh, row + c, mul(G, p.res_scale));
-                F8 w = lds8f(post + 32 * c);
+                F8 w = get_shared(post, p.chunks, c);
                 if (element) {
                     if (p.dgate) {
                         F8 dg = mul(mul(mul(G, y), f1), w);
@@ -495,10 +508,16 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, i
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (col < p.H) {
         const float* src = p.part + size_t(which) * p.H + col;
-#pragma unroll 4
-        for (int b = slice; b < blocks; b += 32) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + size_t(b) * 2 * p.H));
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        constexpr int EACH = MAX_SMS * MAX_BLOCKS_SM / 32;  // all of a slice in flight at once
+        float4 v[EACH];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int b = slice + 32 * i;
+            v[i] = b < blocks ? __ldcg(reinterpret_cast<const float4*>(src + size_t(b) * 2 * p.H)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            s.x += v[i].x; s.y += v[i].y; s.z += v[i].z; s.w += v[i].w;
         }
     }
     sums[slice][q] = s;
@@ -529,9 +548,6 @@ NormShape norm_shape(int H, long long T, int sm_count) {
     return s;
 }
 
-// An upper bound on the blocks of the backward pass that needs no device: the workspace query
-// works without one.
-constexpr int MAX_SMS = 160, MAX_BLOCKS_SM = 2;
 constexpr int TICKET_WORD = 8;  // of the workspace's control block
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

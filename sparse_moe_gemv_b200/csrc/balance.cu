@@ -105,7 +105,7 @@ struct Ring {
     // The mask bytes of LPR groups, a lane each: one load for as many rows of the lane's own.
     __device__ __forceinline__ unsigned look() {
         bool m = row2 < T;
-        if (m && mask) m = __ldg(mask + row2);
+        if (m && mask) m = mask[row2];
         row2 += LPR * step;
         const unsigned all = __ballot_sync(FULL, m);
         return LPR == 32 ? all : (all >> ((threadIdx.x & 31) / LPR * LPR)) & ((1u << (LPR & 31)) - 1u);
@@ -270,12 +270,13 @@ __global__ void __launch_bounds__(32 * WARPS, 1) balance_forward_kernel(const Ba
     const int step = gridDim.x * warps * RPW;
     int t0 = (blockIdx.x * warps + warp) * RPW, t = t0 + lane / LPR;  // the warp's first row, and this lane's
     Ring<DT, VEC, NCH, LPR> ring;
+    wait_for_previous();
     ring.start(p.logits, p.mask, p.T, p.E, p.depth, reinterpret_cast<unsigned char*>(sm) + warp * p.ring_bytes, t0, step);
     for (int e = threadIdx.x; e < p.E; e += threads) hist[e] = 0;
     const int32_t* ids = p.ids + size_t(t) * p.k + l;
     const size_t ids_step = size_t(step) * p.k;
-    int id_next = t < p.T && l < p.k ? __ldg(ids) : -1;
-    asm volatile("griddepcontrol.launch_dependents;");  // the second kernel may take its place to wait
+    int id_next = t < p.T && l < p.k ? *ids : -1;
+    let_next_start();  // the second kernel
     __syncthreads();
 
     float2 acc[N2];
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) balance_forward_kernel(const Ba
     for (; t0 < p.T; t0 += step, t += step) {
         const int id = id_next;
         ids += ids_step;
-        id_next = t + step < p.T && l < p.k ? __ldg(ids) : -1;
+        id_next = t + step < p.T && l < p.k ? *ids : -1;
         bool now;
         float2 v[N2];
         if (!ring.take(p.logits, t0, p.E, v, now)) continue;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) balance_forward_kernel(const Ba
             ++rows;
             if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
             for (int j = l + LPR; j < p.k; j += LPR) {
-                const int more = __ldg(p.ids + size_t(t) * p.k + j);
+                const int more = p.ids[size_t(t) * p.k + j];
                 if (more >= 0 && more < p.E) atomicAdd(&hist[more], 1);
             }
         }
@@ -368,7 +369,8 @@ __global__ void __cluster_dims__(BAL_CLUSTER, 1, 1) __launch_bounds__(FIN_THREAD
     const int quads = padded(p.E) / 4, share = (quads + BAL_CLUSTER - 1) / BAL_CLUSTER;  // 1 .. 32 column groups
     const int q0 = int(rank) * share, mine = max(0, min(share, quads - q0));
     const int parts = FIN_THREADS / share, quad = threadIdx.x % share, part = threadIdx.x / share;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
+    let_next_start();
     float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     int4 c = make_int4(0, 0, 0, 0);
     if (part < parts && quad < mine) {
@@ -498,7 +500,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) balance_backward_kernel(const B
     int t0 = (blockIdx.x * WARPS + warp) * RPW, t = t0 + lane / LPR;
     extern __shared__ __align__(16) unsigned char rings[];
     Ring<DT, VEC, NCH, LPR> ring;
+    wait_for_previous();
     ring.start(p.logits, p.mask, p.T, p.E, p.depth, rings + warp * p.ring_bytes, t0, step);
+    let_next_start();
     const int n = max(*p.n_rows, 1);
     const int mean = int((long long)n * p.k / p.E);
     const float gb = p.grad[0] * (float(p.E) / (float(n) * float(p.k))) / float(n);
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) balance_backward_kernel(const B
 #pragma unroll
     for (int k = 0; k < 2 * N2; ++k) {
         const int e = (l + LPR * (k / VEC)) * VEC + k % VEC;
-        const float c = e < p.E ? float(__ldg(p.counts + e) - mean) : 0.0f;
+        const float c = e < p.E ? float(p.counts[e] - mean) : 0.0f;
         if (k & 1) f[k / 2].y = c;
         else f[k / 2].x = c;
     }
@@ -667,7 +671,7 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     smem = smem > sums ? smem : sums;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!launch(kern, dim3(blocks), 32 * warps, smem, s, false, p)) return REDMOE_ERR_CUDA;
+    if (!launch(kern, dim3(blocks), 32 * warps, smem, s, true, p)) return REDMOE_ERR_CUDA;
     return launch(balance_finish_kernel, dim3(BAL_CLUSTER), FIN_THREADS, 0, s, true, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
@@ -702,7 +706,7 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     const int blocks = balance_blocks(T, rows_a_block(E, BAL_WARPS), di.sm_count);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, false, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
+    return launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, true, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -273,7 +273,7 @@ __device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<P>& c, i
 #pragma unroll
             for (int i = 0; i < EACH; ++i) {
                 const int k = EACH * h + i;
-                reinterpret_cast<uint16_t*>(ss)[k] = k < groups ? __ldg(c.sc + k) : uint16_t(0);
+                reinterpret_cast<uint16_t*>(ss)[k] = k < groups ? c.sc[k] : uint16_t(0);
             }
         }
     }
@@ -396,9 +396,8 @@ __global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(const 
         }
         cp_commit();
     };
-        // launched while the kernel before it ends: nothing is read or written before that has ended
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
+    wait_for_previous();
+    let_next_start();
     const RowShare share(p.T);
     fetch_x(p, share, stride, xs);
     cp_commit();

@@ -11,7 +11,7 @@ namespace redmoe {
 bool allow_smem(const void* kern, int bytes);
 
 // kern(args...). `early`: the blocks may be placed while the kernel before on the stream ends; the
-// kernel waits for that end itself (griddepcontrol.wait).
+// kernel waits for that end itself (wait_for_previous).
 template <class... P, class... A>
 bool launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, bool early, A... args) {
     cudaLaunchAttribute attr[1];
@@ -28,5 +28,14 @@ bool launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaSt
     cudaGetLastError();
     return false;
 }
+
+#ifdef __CUDACC__
+// In a kernel that is launched early, before it reads or writes global memory. What kernels before it
+// wrote is then visible to plain loads; loads through the read-only path (ld.global.nc) are not used
+// in such kernels, since their data would have to stay unchanged from the kernel's start.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on (in all blocks) the next kernel on the stream may take room that is left, to wait there.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+#endif
 
 }  // namespace redmoe

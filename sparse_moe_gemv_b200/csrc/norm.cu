@@ -138,6 +138,8 @@ __global__ void __launch_bounds__(512, 2) norm_forward_kernel(const NormParams p
     if (t >= p.T) return;  // whole groups only: the group barriers stay complete
     const size_t row = size_t(t) * p.chunks;
     clear_unused(red[0][group], red[1][group], RED, lane, p.tpr);
+    wait_for_previous();
+    let_next_start();
 
     Raw8<HD> hr[NC];
     Raw8<YD> yr[NC];
@@ -331,6 +333,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
         in = in == p.ahead ? 0 : in + 1;
         rows_commit();
     };
+    wait_for_previous();
     for (int i = 0; i < p.ahead; ++i) ask(t + i * step);
     shared_vectors(p, BRANCH, dyn, dyn + p.H);
     __syncthreads();
@@ -438,8 +441,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
             }
         }
     }
+    let_next_start();  // norm_columns_kernel, if there is a part
     if (!p.part) return;
-    if (!p.ticket) asm volatile("griddepcontrol.launch_dependents;");  // norm_columns_kernel may take its place to wait
     // the groups' column sums, added in group order by group 0
     __syncthreads();
     if (group > 0) {
@@ -504,7 +507,8 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, i
     const int which = blockIdx.y, q = threadIdx.x & 7, slice = threadIdx.x >> 3;
     if (which == 0 ? !p.want_pre : !(p.want_post || p.want_gate)) return;
     const int col = blockIdx.x * 32 + 4 * q;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
+    let_next_start();
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (col < p.H) {
         const float* src = p.part + size_t(which) * p.H + col;
@@ -701,7 +705,7 @@ redmoe_status redmoe_norm_forward(const redmoe_norm* N, const void* h, const voi
     const long long need = (T + (long long)s.rows - 1) / s.rows;
     const int threads = s.tpr * s.rows;
     const NormKernel kern = pick_forward(N, s.nc, branch);
-    return launch(kern, dim3(unsigned(need)), threads, 0, static_cast<cudaStream_t>(stream), false, p) ? REDMOE_OK
+    return launch(kern, dim3(unsigned(need)), threads, 0, static_cast<cudaStream_t>(stream), true, p) ? REDMOE_OK
                                                                                                        : REDMOE_ERR_CUDA;
 }
 
@@ -795,7 +799,7 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     // counter (5.0 -> 7.2 us); with 16 rows of 2048 it would cost 12.
     const bool one = work && (long long)blocks * p.H <= 4096;
     p.ticket = one ? static_cast<unsigned*>(workspace) + TICKET_WORD : nullptr;
-    if (!launch(kern, dim3(blocks), threads, smem, stm, false, p)) return REDMOE_ERR_CUDA;
+    if (!launch(kern, dim3(blocks), threads, smem, stm, true, p)) return REDMOE_ERR_CUDA;
     if (!work || one) return REDMOE_OK;
     return launch(norm_columns_kernel, dim3((p.H + 31) / 32, 2), 256, 0, stm, true, p, blocks) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }

@@ -123,13 +123,13 @@ struct RawAny {
     uint4 a, b;
     __device__ __forceinline__ void load(const void* p, bool f32, size_t chunk) {
         const uint4* q = static_cast<const uint4*>(p) + (f32 ? 2 * chunk : chunk);
-        a = __ldg(q);
-        if (f32) b = __ldg(q + 1);
+        a = *q;
+        if (f32) b = q[1];
     }
     __device__ __forceinline__ F8 get(bool f32) const { return f32 ? f32x8(a, b) : bf16x8(a); }
 };
 __device__ __forceinline__ float load1(const void* p, bool f32, size_t i) {
-    return f32 ? __ldg(static_cast<const float*>(p) + i) : bf16f(__ldg(static_cast<const uint16_t*>(p) + i));
+    return f32 ? static_cast<const float*>(p)[i] : bf16f(static_cast<const uint16_t*>(p)[i]);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -147,3 +147,72 @@ def test_router_training_step(gpu_lib):
     f = counts.cpu().double() / (T * shape.k)
     (shape.E * (f * p.mean(0)).sum() + 0.1 * torch.logsumexp(ll, 1).pow(2).mean()).backward()
     assert float((dh.cpu().double() - hh.grad).abs().max()) <= 8 * 2.0 ** -8 * float(hh.grad.abs().max())
+
+
+@pytest.mark.parametrize("T,H", [(1, 264), (37, 264), (300, 2048)])
+def test_calls_that_follow_one_another_closely(gpu_lib, T, H):
+    """A call's kernel may be placed while the one before it ends. A chain in which each call reads or
+    overwrites what the ones before it read or wrote (rows that end inside a sector, in place, with copies
+    and fills between, over two streams) equals the same calls one at a time, eager and captured."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + H)
+
+    def rnd(*s, dt=torch.bfloat16):
+        return torch.randn(*s, generator=g, device="cuda").to(dt)
+
+    step = smg.Norm(H, y_dtype="bf16", pre_w=rnd(H), post_w=rnd(H), gate="element", gate_act="sigmoid", res_scale=0.5)
+    wide = smg.Norm(H, pre_w=rnd(H))
+    n = -(-H // 32) * 32
+    mats = [smg.Matrix(*mi.quantize_int4g32(torch.randn(H, n, generator=g, device="cuda")), H, n) for _ in range(2)]
+    E, k, rows = 61, 3, min(T, 32)
+    first = {"h": rnd(T, H), "y": rnd(T, H), "x": rnd(T, H), "gate": rnd(T, H), "in": rnd(rows, n), "lg": rnd(T, E, dt=torch.float32)}
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    ws, wb = smg.new_norm_workspace(step, T), smg.new_balance_workspace(T, E)
+    side = torch.cuda.Stream()
+
+    def chain(s, wait):
+        out = {"dh": torch.empty_like(s["h"]), "dy": torch.empty_like(s["y"]), "dg": torch.empty_like(s["gate"]),
+               "dpre": torch.empty(H, device="cuda"), "dpost": torch.empty(H, device="cuda")}
+        loss, prob = torch.empty(2, device="cuda"), torch.empty(E, device="cuda")
+        counts, nr = torch.empty(E, device="cuda", dtype=torch.int32), torch.empty(1, device="cuda", dtype=torch.int32)
+        coef = torch.ones(2, device="cuda")
+        for i in range(6):
+            for j in range(3):
+                smg.redmoe_norm_forward(step, s["h"], h_out=s["h"], x=s["x"], y=s["y"], gate=s["gate"])
+                wait()
+            s["in"].zero_()
+            s["in"][:, :H].copy_(s["x"][:rows])
+            wait()
+            smg.redmoe_gemv(mats[i % 2], s["in"], s["y"][:rows])   # the next step's y
+            wait()
+            smg.redmoe_norm_backward(step, s["h"], out["dh"], ws, dh_out=s["x"], dx=s["gate"], y=s["y"], gate=s["gate"],
+                                     dy=out["dy"], dgate=out["dg"], dpost_w=out["dpost"], dpre_w=out["dpre"])
+            wait()
+            side.wait_stream(torch.cuda.current_stream())
+            smg.redmoe_balance_forward(s["lg"], ids, loss, counts, prob, nr, wb, stream=side)
+            smg.redmoe_balance_backward(s["lg"], counts, nr, coef, s["lg"], k, stream=side)   # in place
+            wait()
+            smg.redmoe_norm_forward(wide, out["dh"], x=s["gate"])   # the next step's gate
+            torch.cuda.current_stream().wait_stream(side)
+            wait()
+            smg.redmoe_balance_backward(s["lg"], counts, nr, coef, s["lg"], k)
+            wait()
+        return {**s, **out, "loss": loss, "counts": counts, "prob": prob}
+
+    want = chain({k_: v.clone() for k_, v in first.items()}, torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    got = chain({k_: v.clone() for k_, v in first.items()}, lambda: None)
+    torch.cuda.synchronize()
+    assert all(bool(v.isfinite().all()) for v in want.values())
+    assert all(torch.equal(got[n_], want[n_]) for n_ in want), [n_ for n_ in want if not torch.equal(got[n_], want[n_])]
+    held = {k_: v.clone() for k_, v in first.items()}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(held, lambda: None)
+    for _ in range(3):
+        for n_, v in first.items():
+            held[n_].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[n_], want[n_]) for n_ in want), [n_ for n_ in want if not torch.equal(got[n_], want[n_])]

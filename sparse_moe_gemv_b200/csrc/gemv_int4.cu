@@ -37,8 +37,9 @@
 // waits for another until the end, and the loads in flight need no registers.
 //
 // Measured on a B200: 151936 x 2048 at one token 34.2 us (26.7 at the copy bandwidth; the steady rate
-// is 93% of it, five to six us are the launch, x and the last steps). 24571 x 4096 at 13 tokens 24.4
-// us (8.6): bound by the reads of x from shared memory, which every 16 rows of W repeat.
+// is 93% of it, five to six us are the launch, x and the last steps). 24571 x 4096 at 13 tokens 23.9
+// us (8.6): 60% of the copy bandwidth in the steady state, where the reads of x from shared memory
+// keep that four fifths busy, and ten us for the launch, x (1.7 to fetch, 2.5 to shape) and the tail.
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -198,7 +199,7 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
 //          tiles of 256 or 128 columns take 31.9 and 29.7, one tile 24.5 (T = 13, 24571 x 4096)
 //   WARPS  20 and 16: 34.2 (T = 1, 151936 x 2048) and 16.4 (T = 4); 12 warps 37.8 and 18.0
 //   COLS   512 at one token 35.1 (151936 x 2048), 256 37.5
-//   SLOTS  2: 34.2, 16.4, 24.4, 26.3 (T = 1, 4, 13; T = 32 at 24571 x 2048), 3: 36.8, 17.7, 26.5,
+//   SLOTS  2: 34.2, 16.4, 24.4, 26.3 us (T = 1, 4, 13; T = 32 at 24571 x 2048), 3: 36.8, 17.7, 26.5,
 //          30.2: what a third slot asks for first costs more than the second leaves open
 template <int NT, int M_ = 1> struct Plan {
     static constexpr bool ONE = NT == 0;

@@ -22,8 +22,9 @@
 // threads (whole warps, eight or sixteen columns a thread) that holds it on chip, so the
 // statistics cost reductions over the group and nothing is read twice. All sums are fp32, in a
 // fixed order. Measured on a B200, of the copy bandwidth: forward 8191 x 5120 fp32 with an element
-// gate 106 us (84%), 8192 x 4096 47 us (86%), 2048 x 2048 12.1 us (53%: under two waves of blocks),
-// one row of 2048 1.8 us; backward 8192 x 2048 48 us (63%: some sixty instructions an element).
+// gate 106 us (84%), 8192 x 4096 47 us (86%), 2048 x 2048 11.8 us (54%: under two waves of blocks),
+// one row of 2048 1.45 us; backward 8192 x 2048 47 us (65%: 79% in the steady state, nine us are the
+// launches, the first rows and the column sums).
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -539,10 +540,10 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p, i
 struct NormShape {
     int nc, tpr, rows;  // chunks a thread, threads a row, rows a block
 };
-// A thread has one chunk of a row while the rows' blocks are few (the shortest way through a row:
-// 1.9 against 2.3 us for one row of 2048), two where they are many (half the threads at a barrier,
-// twice the loads in flight of each: 25.9 against 32.9 us for 8192 rows of 2048) and where 512
-// threads would not do.
+// A thread has one chunk of a row while the rows' warps find room on the device at once (the shortest
+// way through a row: 512 rows of 2048 take 3.4 us, 3.7 with two), two where they do not (half the
+// threads at a barrier, twice the loads in flight of each: 1024 rows 5.2 against 6.0, 4096 rows 16.1
+// against 17.5) and where 512 threads would not do.
 NormShape norm_shape(int H, long long T, int sm_count) {
     NormShape s;
     const int chunks = H / 8;

@@ -36,8 +36,8 @@
 // into a ring of its own with asynchronous copies (128-byte lines asked for whole), so no warp
 // waits for another until the end, and the loads in flight need no registers.
 //
-// Measured on a B200: 151936 x 2048 at one token 34.2 us (26.7 at the copy bandwidth; the steady rate
-// is 93% of it, five to six us are the launch, x and the last steps). 24571 x 4096 at 13 tokens 23.9
+// Measured on a B200: 151936 x 2048 at one token 33.1 us (26.7 at the copy bandwidth; the steady rate
+// is 93% of it, four to five us are the launch, x and the last steps). 24571 x 4096 at 13 tokens 23.9
 // us (8.6): 60% of the copy bandwidth in the steady state, where the reads of x from shared memory
 // keep that four fifths busy, and ten us for the launch, x (1.7 to fetch, 2.5 to shape) and the tail.
 #include "common.cuh"
@@ -412,9 +412,9 @@ __global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(const 
     const unsigned char* x0[NX];
     int xstep[NX];  // bytes a step adds
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
+    for (int i = 0; i < NX; ++i) {  // one token: zeros 32 bytes on, in other banks than x's (33.1 against 34.3 us, as above)
         const bool there = ONE ? (g & 3) == q : 8 * i + g < p.T;  // one token: this lane is its column's group
-        x0[i] = (there ? xs + (ONE ? 64 * g : (8 * i + g) * stride) : zero) + (ONE ? 0 : 16 * q);
+        x0[i] = there ? xs + (ONE ? 64 * g : (8 * i + g) * stride + 16 * q) : zero + (ONE ? 32 : 16 * q);
         xstep[i] = there ? 2 * P::COLS : 0;
     }
     const unsigned char* my_w = ring + (ONE ? (lane / 8) * P::WROW + 16 * (lane % 8) : g * P::WROW + 4 * q);

@@ -462,6 +462,9 @@ def _arg(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, dev: i
     return t.data_ptr()
 
 
+_INT32_MAX = 2**31 - 1
+
+
 def _int32(n: int, name: str) -> int:
     """A size that the library takes as int32 (ctypes would cut a longer one silently)."""
     if not -2**31 <= n < 2**31:
@@ -485,15 +488,11 @@ def _work(workspace: Optional[torch.Tensor], dev: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(fn, where: str, dev: int, stream, *args) -> None:
-    """fn(*args, stream) with `dev` current; the default stream is dev's current one."""
-    if dev == _raw_device():  # a tensor on dev: CUDA is initialised
-        st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
-    if st != 0:
-        raise RedmoeError(st, where)
+# The calls below are short beside what Python adds to them, so each is written out: a call for another
+# device than the current one starts over with that device current, and every attribute is read once.
+def _elsewhere(dev: int, fn, *args, **kw) -> None:
+    with torch.cuda.device(dev):
+        fn(*args, **kw)
 
 
 class Norm:
@@ -548,13 +547,21 @@ def redmoe_norm_forward(norm: Norm, h: torch.Tensor, h_out: Optional[torch.Tenso
                         x: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                         gate: Optional[torch.Tensor] = None, stream=None) -> None:
     """x <- N(h) (no y), or h_out [T,H] (may be h) and, where given, x [T,H] <- the residual step on (h, y)."""
-    dev, T = norm._dev(h, "h"), _int32(h.size(0), "T")
-    rows, ht = (T, norm.hidden), norm.h_torch
-    _call((_lib or load()).redmoe_norm_forward, "redmoe_norm_forward", dev, stream, norm.ref, _arg(h, "h", rows, ht, dev),
-          None if y is None else _arg(y, "y", rows, norm.y_torch, dev),
-          None if gate is None else _arg(gate, "gate", norm.gate_shape(T), norm.gate_torch, dev), T,
-          None if h_out is None else _arg(h_out, "h_out", rows, ht, dev),
-          None if x is None else _arg(x, "x", rows, norm.x_torch, dev))
+    dev = norm._dev(h, "h")
+    if dev != _raw_device():  # a tensor on a device: CUDA is initialised
+        return _elsewhere(dev, redmoe_norm_forward, norm, h, h_out, x, y, gate, stream)
+    rows, ht = h.shape, norm.h_torch
+    T = rows[0] if rows else 0
+    if T > _INT32_MAX or rows != (T, norm.hidden):
+        rows = (_int32(T, "T"), norm.hidden)
+    st = (_lib or load()).redmoe_norm_forward(
+        norm.ref, _arg(h, "h", rows, ht, dev), None if y is None else _arg(y, "y", rows, norm.y_torch, dev),
+        None if gate is None else _arg(gate, "gate", norm.gate_shape(T), norm.gate_torch, dev), T,
+        None if h_out is None else _arg(h_out, "h_out", rows, ht, dev),
+        None if x is None else _arg(x, "x", rows, norm.x_torch, dev),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise RedmoeError(st, "redmoe_norm_forward")
 
 
 def redmoe_norm_workspace_bytes(norm: Norm, T: int) -> int:
@@ -579,19 +586,28 @@ def redmoe_norm_backward(norm: Norm, h_out: torch.Tensor, dh: torch.Tensor, work
                          stream=None) -> None:
     """dh, dy, dgate, dpost_w and dpre_w (fp32 [H]) <- the gradients dh_out and dx that arrive at
     h_out and x. dgate is fp32 for a token or channel gate, the gate's dtype for an element gate."""
-    dev, T = norm._dev(h_out, "h_out"), _int32(h_out.size(0), "T")
-    rows, cols, f32 = (T, norm.hidden), (norm.hidden,), torch.float32
+    dev = norm._dev(h_out, "h_out")
+    if dev != _raw_device():
+        return _elsewhere(dev, redmoe_norm_backward, norm, h_out, dh, workspace, dh_out, dx, y, gate, dy, dgate, dpost_w,
+                          dpre_w, stream)
+    T = _int32(h_out.size(0), "T")
+    rows, cols, f32, ht = (T, norm.hidden), (norm.hidden,), torch.float32, norm.h_torch
     g = dg = None
     if gate is not None:
         g = _arg(gate, "gate", norm.gate_shape(T), norm.gate_torch, dev)
     if dgate is not None:
         dg = _arg(dgate, "dgate", norm.gate_shape(T), norm.gate_torch if norm.gate == "element" else f32, dev)
     ws, nbytes = _work(workspace, dev)
-    _call((_lib or load()).redmoe_norm_backward, "redmoe_norm_backward", dev, stream, norm.ref,
-          _arg(h_out, "h_out", rows, norm.h_torch, dev), _arg(y, "y", rows, norm.y_torch, dev), g,
-          _arg(dh_out, "dh_out", rows, norm.h_torch, dev), _arg(dx, "dx", rows, norm.x_torch, dev), T,
-          _arg(dh, "dh", rows, norm.h_torch, dev), _arg(dy, "dy", rows, norm.y_torch, dev), dg,
-          _arg(dpost_w, "dpost_w", cols, f32, dev), _arg(dpre_w, "dpre_w", cols, f32, dev), ws, nbytes)
+    st = (_lib or load()).redmoe_norm_backward(
+        norm.ref, _arg(h_out, "h_out", rows, ht, dev), None if y is None else _arg(y, "y", rows, norm.y_torch, dev), g,
+        None if dh_out is None else _arg(dh_out, "dh_out", rows, ht, dev),
+        None if dx is None else _arg(dx, "dx", rows, norm.x_torch, dev), T, _arg(dh, "dh", rows, ht, dev),
+        None if dy is None else _arg(dy, "dy", rows, norm.y_torch, dev), dg,
+        None if dpost_w is None else _arg(dpost_w, "dpost_w", cols, f32, dev),
+        None if dpre_w is None else _arg(dpre_w, "dpre_w", cols, f32, dev), ws, nbytes,
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise RedmoeError(st, "redmoe_norm_backward")
 
 
 def redmoe_workspace_bytes_block(layer: Layer, T: int) -> int:
@@ -612,19 +628,25 @@ def redmoe_forward_block(layer: Layer, before: Norm, after: Norm, h: torch.Tenso
                          stream=None) -> None:
     """The residual block around the layer: x = N(h) by `before`, y = layer(x), then `after`'s step on
     (h, y) into h_out (may be h) and, where given, x_next."""
-    dev, T = before._dev(h, "h"), _int32(h.size(0), "T")
+    dev = before._dev(h, "h")
     after._dev(h, "h")
+    if dev != _raw_device():
+        return _elsewhere(dev, redmoe_forward_block, layer, before, after, h, h_out, topk_ids, topk_w, workspace, x_next,
+                          gate, stream)
+    T = _int32(h.size(0), "T")
     for name, t in layer.tensors.items():
         if t is not None and t.get_device() != dev:
             raise ValueError(f"the layer's {name} is on {t.device}, h on cuda:{dev}")
     rows, picks = (T, layer.hidden), (T, layer.top_k)
     ws, nbytes = _work(workspace, dev)
-    _call((_lib or load()).redmoe_forward_block, "redmoe_forward_block", dev, stream, layer.ref, before.ref, after.ref,
-          _arg(h, "h", rows, before.h_torch, dev),
-          None if gate is None else _arg(gate, "gate", after.gate_shape(T), after.gate_torch, dev), T,
-          _arg(h_out, "h_out", rows, after.h_torch, dev), _arg(x_next, "x_next", rows, after.x_torch, dev),
-          _arg(topk_ids, "topk_ids", picks, torch.int32, dev), _arg(topk_w, "topk_w", picks, torch.float32, dev),
-          ws, nbytes)
+    st = (_lib or load()).redmoe_forward_block(
+        layer.ref, before.ref, after.ref, _arg(h, "h", rows, before.h_torch, dev),
+        None if gate is None else _arg(gate, "gate", after.gate_shape(T), after.gate_torch, dev), T,
+        _arg(h_out, "h_out", rows, after.h_torch, dev), _arg(x_next, "x_next", rows, after.x_torch, dev),
+        _arg(topk_ids, "topk_ids", picks, torch.int32, dev), _arg(topk_w, "topk_w", picks, torch.float32, dev),
+        ws, nbytes, _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise RedmoeError(st, "redmoe_forward_block")
 
 
 def redmoe_balance_workspace_bytes(T: int, n_experts: int) -> int:
@@ -640,12 +662,14 @@ def new_balance_workspace(T: int, n_experts: int, device=None) -> torch.Tensor:
 
 
 def _logits(logits: torch.Tensor):
-    dev = _device_of(logits, "logits")
-    code = _CODES.get(logits.dtype)
-    if code is None or logits.dim() != 2 or not logits.is_contiguous():
+    dev, code, shape = _device_of(logits, "logits"), _CODES.get(logits.dtype), logits.shape
+    if code is None or len(shape) != 2 or not logits.is_contiguous():
         raise ValueError(f"logits: expected a contiguous float32 or bfloat16 [T, E] tensor, got {logits.dtype} "
                          f"{list(logits.shape)}")
-    return dev, code, _int32(logits.shape[0], "T"), _int32(logits.shape[1], "E")
+    T, E = shape
+    if T > _INT32_MAX or E > _INT32_MAX:
+        _int32(max(T, E), "a size of logits")
+    return dev, code, T, E
 
 
 def _mask(mask: Optional[torch.Tensor], T: int, dev: int):
@@ -660,15 +684,20 @@ def redmoe_balance_forward(logits: torch.Tensor, topk_ids: torch.Tensor, loss: t
     """loss[2] fp32 (balance, z), counts[E] int32, prob[E] fp32, n_rows[1] int32 <- the rows of logits
     [T,E] and topk_ids [T,k] int32 whose mask byte [T] (uint8 or bool) is not zero."""
     dev, code, T, E = _logits(logits)
+    if dev != _raw_device():
+        return _elsewhere(dev, redmoe_balance_forward, logits, topk_ids, loss, counts, prob, n_rows, workspace, mask, stream)
     if topk_ids.dim() != 2:
         raise ValueError(f"topk_ids: expected [T, k], got {list(topk_ids.shape)}")
     k = _int32(topk_ids.shape[1], "k")
     f32, i32 = torch.float32, torch.int32
     ws, nbytes = _work(workspace, dev)
-    _call((_lib or load()).redmoe_balance_forward, "redmoe_balance_forward", dev, stream, logits.data_ptr(), code,
-          _arg(topk_ids, "topk_ids", (T, k), i32, dev), _mask(mask, T, dev), T, E, k, _arg(loss, "loss", (2,), f32, dev),
-          _arg(counts, "counts", (E,), i32, dev), _arg(prob, "prob", (E,), f32, dev),
-          _arg(n_rows, "n_rows", (1,), i32, dev), ws, nbytes)
+    st = (_lib or load()).redmoe_balance_forward(
+        logits.data_ptr(), code, _arg(topk_ids, "topk_ids", (T, k), i32, dev),
+        None if mask is None else _mask(mask, T, dev), T, E, k, _arg(loss, "loss", (2,), f32, dev),
+        _arg(counts, "counts", (E,), i32, dev), _arg(prob, "prob", (E,), f32, dev),
+        _arg(n_rows, "n_rows", (1,), i32, dev), ws, nbytes, _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise RedmoeError(st, "redmoe_balance_forward")
 
 
 def redmoe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, n_rows: torch.Tensor, grad_loss: torch.Tensor,
@@ -677,10 +706,16 @@ def redmoe_balance_backward(logits: torch.Tensor, counts: torch.Tensor, n_rows: 
     """dlogits [T,E] (the logits' dtype; may be logits) <- grad_loss[2] fp32, with the forward call's
     counts, n_rows and mask."""
     dev, code, T, E = _logits(logits)
-    _call((_lib or load()).redmoe_balance_backward, "redmoe_balance_backward", dev, stream, logits.data_ptr(), code,
-          _mask(mask, T, dev), T, E, _int32(top_k, "top_k"), _arg(counts, "counts", (E,), torch.int32, dev),
-          _arg(n_rows, "n_rows", (1,), torch.int32, dev), _arg(grad_loss, "grad_loss", (2,), torch.float32, dev),
-          _arg(dlogits, "dlogits", (T, E), logits.dtype, dev))
+    if dev != _raw_device():
+        return _elsewhere(dev, redmoe_balance_backward, logits, counts, n_rows, grad_loss, dlogits, top_k, mask, stream)
+    i32 = torch.int32
+    st = (_lib or load()).redmoe_balance_backward(
+        logits.data_ptr(), code, None if mask is None else _mask(mask, T, dev), T, E, _int32(top_k, "top_k"),
+        _arg(counts, "counts", (E,), i32, dev), _arg(n_rows, "n_rows", (1,), i32, dev),
+        _arg(grad_loss, "grad_loss", (2,), torch.float32, dev), _arg(dlogits, "dlogits", (T, E), logits.dtype, dev),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise RedmoeError(st, "redmoe_balance_backward")
 
 
 class Matrix:
@@ -688,10 +723,10 @@ class Matrix:
     and bf16 scales s [rows, cols/32], kept alive by this object."""
 
     def __init__(self, w: torch.Tensor, s: torch.Tensor, rows: int, cols: int, dtype: str = "int4g32"):
+        self.device = _device_of(w, "w")
         if dtype == "int4g32":  # other formats are refused by the call
-            dev = _device_of(w, "w")
-            _arg(w, "w", (rows, cols // 2), torch.uint8, dev)
-            _arg(s, "s", (rows, cols // 32), torch.bfloat16, dev)
+            _arg(w, "w", (rows, cols // 2), torch.uint8, self.device)
+            _arg(s, "s", (rows, cols // 32), torch.bfloat16, self.device)
         _int32(rows, "rows"), _int32(cols, "cols")
         st = _Matrix()
         st.rows, st.cols, st.dtype, st.w, st.s = rows, cols, DTYPES[dtype], _ptr(w), _ptr(s)
@@ -701,9 +736,17 @@ class Matrix:
 
 def redmoe_gemv(matrix: Matrix, x: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """y[T, rows] (fp32 or bf16) <- x[T, cols] bf16 times the matrix's transpose, T = 0..32."""
-    dev = _device_of(matrix.w, "w")
-    T = _int32(x.size(0), "T")
-    if x.dtype not in _CODES or y.dtype not in _CODES:
-        raise ValueError(f"x and y are float32 or bfloat16: got {x.dtype} and {y.dtype}")
-    _call((_lib or load()).redmoe_gemv, "redmoe_gemv", dev, stream, matrix.ref, _arg(x, "x", (T, matrix.cols), x.dtype, dev),
-          _CODES[x.dtype], T, _arg(y, "y", (T, matrix.rows), y.dtype, dev), _CODES[y.dtype])
+    dev = matrix.device
+    if dev != _raw_device():
+        return _elsewhere(dev, redmoe_gemv, matrix, x, y, stream)
+    xt, yt, T = x.dtype, y.dtype, x.size(0)
+    xc, yc = _CODES.get(xt), _CODES.get(yt)
+    if xc is None or yc is None:
+        raise ValueError(f"x and y are float32 or bfloat16: got {xt} and {yt}")
+    if T > _INT32_MAX:
+        _int32(T, "T")
+    st = (_lib or load()).redmoe_gemv(matrix.ref, _arg(x, "x", (T, matrix.cols), xt, dev), xc, T,
+                                      _arg(y, "y", (T, matrix.rows), yt, dev), yc,
+                                      _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise RedmoeError(st, "redmoe_gemv")

@@ -364,9 +364,8 @@ redmoe_status redmoe_norm_forward(const redmoe_norm *N, const void *h, const voi
  *            not wanted
  *   dpost_w, dpre_w   fp32 [hidden], 16-byte aligned; NULL: not wanted
  * Overwritten, not accumulated; sums over rows are fp32 in a fixed order. The workspace is
- * needed for dpost_w, dpre_w and a CHANNEL dgate (else it may be NULL) and starts with the
- * usual control block (zero before the first use, left zero). T == 0 zeroes those three and
- * touches nothing else. */
+ * needed for dpost_w, dpre_w and a CHANNEL dgate (else it may be NULL); its control block is
+ * not used. T == 0 zeroes those three and touches nothing else. */
 size_t redmoe_norm_workspace_bytes(const redmoe_norm *N, int32_t T);
 redmoe_status redmoe_norm_backward(const redmoe_norm *N, const void *h_out, const void *y, const void *gate,
                                    const void *dh_out, const void *dx, int32_t T, void *dh, void *dy, void *dgate,

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) balance_forward_kernel(const Ba
 // The second kernel: rank r of the cluster adds the blocks' sums of its share of the columns, every
 // thread four columns of every parts-th block, then the parts in order; rank 0 makes the losses.
 constexpr int FIN_THREADS = 1024;
-__global__ void __cluster_dims__(BAL_CLUSTER, 1, 1) __launch_bounds__(FIN_THREADS) balance_finish_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(FIN_THREADS) balance_finish_kernel(const BalanceParams p) {
     __shared__ float4 fsum[FIN_THREADS];
     __shared__ int4 csum[FIN_THREADS];
     __shared__ double zsum[32];
@@ -671,8 +671,8 @@ redmoe_status redmoe_balance_forward(const void* logits, int32_t logits_dtype, c
     smem = smem > sums ? smem : sums;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!launch(kern, dim3(blocks), 32 * warps, smem, s, true, p)) return REDMOE_ERR_CUDA;
-    return launch(balance_finish_kernel, dim3(BAL_CLUSTER), FIN_THREADS, 0, s, true, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
+    if (!launch(kern, dim3(blocks), 32 * warps, smem, s, 1, p)) return REDMOE_ERR_CUDA;
+    return launch(balance_finish_kernel, dim3(BAL_CLUSTER), FIN_THREADS, 0, s, BAL_CLUSTER, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, const uint8_t* row_mask, int32_t T,
@@ -706,7 +706,7 @@ redmoe_status redmoe_balance_backward(const void* logits, int32_t logits_dtype, 
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     const int blocks = balance_blocks(T, rows_a_block(E, BAL_WARPS), di.sm_count);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, true, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
+    return launch(kern, dim3(blocks), 32 * BAL_WARPS, smem, s, 1, p) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 }  // extern "C"

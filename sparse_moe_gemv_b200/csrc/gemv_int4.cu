@@ -516,7 +516,7 @@ bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
     const auto kern = gemv_kernel<NT, M, F32, WHOLE>;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return false;
     const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
-    return launch(kern, dim3(tiles < di.sm_count ? tiles : di.sm_count), 32 * warps, smem, stream, true, p);
+    return launch(kern, dim3(tiles < di.sm_count ? tiles : di.sm_count), 32 * warps, smem, stream, 1, p);
 }
 
 // Whether up to eight tokens take steps of two tiles: where all warps' rings fit beside x (24571 x

@@ -23,8 +23,8 @@
 // statistics cost reductions over the group and nothing is read twice. All sums are fp32, in a
 // fixed order. Measured on a B200, of the copy bandwidth: forward 8191 x 5120 fp32 with an element
 // gate 106 us (84%), 8192 x 4096 47 us (86%), 2048 x 2048 11.8 us (54%: under two waves of blocks),
-// one row of 2048 1.45 us; backward 8192 x 2048 47 us (65%: 79% in the steady state, nine us are the
-// launches, the first rows and the column sums).
+// one row of 2048 1.45 us; backward 8192 x 2048 42.4 us (72%: 95% in
+// the steady state, ten us are launches, first rows and column sums), one row of 2048 4.2 us.
 #include "common.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -57,7 +57,7 @@ struct NormParams {
     int units, ahead;  // walked rows: 16-byte units of a chunk, rows in flight (0 .. 2)
     bool want_pre, want_post, want_gate;
     float *dpre_w, *dpost_w;
-    unsigned* ticket;   // backward: blocks that are done, where the last one adds the column sums; else NULL
+    bool cluster;       // backward: the grid is one cluster, whose blocks add the column sums among themselves
 };
 
 // The sum over a group: warps by shuffles, then the warps' sums through shared memory, four to a lane
@@ -292,6 +292,18 @@ __device__ __forceinline__ void finish_post(const NormParams& p, int c, float a)
     if (p.want_post) p.dpost_w[c] = p.gate_kind == GATE_TOKEN || p.gate_kind == GATE_ELEMENT ? a : a * v;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t at, unsigned rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // Backward. The sums that a row needs are six, all of what is read:
 //   S = {h^2, dx pre h, y^2, dh_out e, dx pre e, h e},  e = y post (times an element gate)
 // since sum G e = S3 + r2 (S4 - k2 S5) with k2 = r2^2 S1 / H: one reduction a row, where summing G e
@@ -458,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
     }
     __syncthreads();
     if (group == 0) {
-        float* out = p.part + size_t(blockIdx.x) * 2 * p.H;
+        float* out = p.cluster ? dyn : p.part + size_t(blockIdx.x) * 2 * p.H;  // dyn: over what this thread has read
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
@@ -472,32 +484,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
                     acc_post[i].v[j] = __fadd2_rn(acc_post[i].v[j], v.v[j]);
                 }
             }
-            if (p.want_pre) store8<DT_F32>(out, c, acc_pre[i]);
-            if (p.want_post || p.want_gate) store8<DT_F32>(out + p.H, c, acc_post[i]);
+            if (p.cluster || p.want_pre) store8<DT_F32>(out, c, acc_pre[i]);
+            if (p.cluster || p.want_post || p.want_gate) store8<DT_F32>(out + p.H, c, acc_post[i]);
         }
     }
-    if (!p.ticket) return;
-    // few partial rows: the block that is last to finish adds them, in block order
-    __shared__ bool last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-        if (last) *p.ticket = 0;
-    }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+    if (!p.cluster) return;
+    // every block adds a share of the columns over the blocks, in block order
+    cluster_sync();
+    const int share = (p.H + gridDim.x - 1) / gridDim.x, c0 = int(blockIdx.x) * share, c1 = min(c0 + share, p.H);
+    for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) {
         float a = 0.0f, b = 0.0f;
-#pragma unroll 4
-        for (unsigned i = 0; i < gridDim.x; ++i) {
-            if (p.want_pre) a += __ldcg(p.part + size_t(i) * 2 * p.H + c);
-            if (p.want_post || p.want_gate) b += __ldcg(p.part + size_t(i) * 2 * p.H + p.H + c);
+#pragma unroll 8
+        for (unsigned r = 0; r < gridDim.x; ++r) {
+            a += ld_cluster(post + 4 * c, r);
+            b += ld_cluster(post + 4 * (p.H + c), r);
         }
         if (p.want_pre) p.dpre_w[c] = a;
-        finish_post(p, c, b);
+        if (p.want_post || p.want_gate) finish_post(p, c, b);
     }
+    cluster_sync();  // no block leaves while another reads its sums
 }
 
 // dpre_w[col] = sum over blocks of part[block][0][col]; A[col] likewise from part[block][1] gives
@@ -553,7 +558,7 @@ NormShape norm_shape(int H, long long T, int sm_count) {
     return s;
 }
 
-constexpr int TICKET_WORD = 8;  // of the workspace's control block
+constexpr int MAX_CLUSTER = 8;  // blocks that add their column sums among themselves
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -706,7 +711,7 @@ redmoe_status redmoe_norm_forward(const redmoe_norm* N, const void* h, const voi
     const long long need = (T + (long long)s.rows - 1) / s.rows;
     const int threads = s.tpr * s.rows;
     const NormKernel kern = pick_forward(N, s.nc, branch);
-    return launch(kern, dim3(unsigned(need)), threads, 0, static_cast<cudaStream_t>(stream), true, p) ? REDMOE_OK
+    return launch(kern, dim3(unsigned(need)), threads, 0, static_cast<cudaStream_t>(stream), 1, p) ? REDMOE_OK
                                                                                                        : REDMOE_ERR_CUDA;
 }
 
@@ -789,20 +794,23 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     p.want_gate = dgate != nullptr && channel;
     const int threads = s.tpr * s.rows, want = threads <= 256 ? MAX_BLOCKS_SM : 1;
     const long long all = (T + (long long)s.rows - 1) / s.rows, most = want * (di.sm_count < MAX_SMS ? di.sm_count : MAX_SMS);
-    const int blocks = int(all < most ? all : most);
+    // Where eight blocks have no more than two of their rows each, they are one cluster that adds its
+    // column sums itself: 4.2 against 4.7 us for one row of 2048, and a launch less for the host (about
+    // 2.5 us a call). 16 rows of 2048 take 5.3 instead of 4.9, as the host's 2.5 are worth.
+    p.cluster = work && all <= 2 * MAX_CLUSTER;
+    int blocks = int(all < most ? all : most);
+    if (p.cluster) {
+        blocks = 1;
+        while (blocks < all && blocks < MAX_CLUSTER) blocks *= 2;  // those without rows add zeros
+    }
     p.units = 2 * units(N->h_dtype) + units(N->x_dtype) + (branch ? units(N->y_dtype) : 0) +
               (branch && N->gate_kind == GATE_ELEMENT ? units(N->gate_dtype) : 0);
     const int smem = rows_smem(p, s, want, di.max_smem_optin);
     const NormKernel kern = pick_backward(N, s.nc, threads, branch);
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
-    // Up to so many partial sums the last block adds them itself. That saves the host a launch (13.0
-    // -> 10.7 us a call of 37 rows of 264 from Python) and costs the GPU 2 us behind a fence and a
-    // counter (5.0 -> 7.2 us); with 16 rows of 2048 it would cost 12.
-    const bool one = work && (long long)blocks * p.H <= 4096;
-    p.ticket = one ? static_cast<unsigned*>(workspace) + TICKET_WORD : nullptr;
-    if (!launch(kern, dim3(blocks), threads, smem, stm, true, p)) return REDMOE_ERR_CUDA;
-    if (!work || one) return REDMOE_OK;
-    return launch(norm_columns_kernel, dim3((p.H + 31) / 32, 2), 256, 0, stm, true, p, blocks) ? REDMOE_OK : REDMOE_ERR_CUDA;
+    if (!launch(kern, dim3(blocks), threads, smem, stm, p.cluster ? blocks : 1, p)) return REDMOE_ERR_CUDA;
+    if (!work || p.cluster) return REDMOE_OK;
+    return launch(norm_columns_kernel, dim3((p.H + 31) / 32, 2), 256, 0, stm, 1, p, blocks) ? REDMOE_OK : REDMOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -227,8 +227,8 @@ def test_same_bits_twice_on_another_stream_and_in_a_graph(gpu_lib):
 
 @pytest.mark.parametrize("T,H", [(5, 264), (37, 64), (300, 16), (64, 2048)])
 def test_repeated_calls_with_one_workspace(gpu_lib, T, H):
-    """Few sums are added by the last block, more by a second kernel: both leave the control block zero
-    and the same workspace serves the next call, other sizes, gradients left out and replays included."""
+    """A few blocks' sums are added within a cluster, more by a second kernel: both leave the control block
+    zero and the same workspace serves the next call, other sizes, gradients left out and replays included."""
     norm, t, kw = make(T, H, post=True, kind="channel")
     first = backward(norm, t, T, H)
     ws = smg.new_norm_workspace(norm, T)

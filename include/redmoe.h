@@ -428,8 +428,8 @@ redmoe_status redmoe_balance_backward(const void *logits, int32_t logits_dtype, 
  * rounding is in proportion to 16 times the sum of |scale x|, since they run over the stored
  * nibbles 0 .. 15. A row of x that holds an infinity or a NaN makes its row of y NaN; other rows
  * are not affected. W is read once for all rows of x if they fit on a multiprocessor (at T = 8
- * up to 10752 columns, at 16 up to 5120, at 32 up to 2304), else once for every equal share of them
- * that does. y must not overlap x or W. */
+ * up to 10752 columns, at 16 up to 5120, at 32 up to 2304), else, and where a matrix of few rows leaves
+ * multiprocessors free, once for every equal share of them. y must not overlap x or W. */
 typedef struct redmoe_matrix {
     int32_t rows;            /* N                                                             */
     int32_t cols;            /* K                                                             */

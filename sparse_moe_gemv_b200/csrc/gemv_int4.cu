@@ -61,6 +61,7 @@ struct GemvParams {
     const uint16_t* x;     // [T, K] bf16
     void* y;               // [T, N]
     int N, K, T;
+    int share;             // tokens of a row of blocks: row blockIdx.y has those from share * blockIdx.y on
 };
 
 __host__ __device__ __forceinline__ int row_stride(int K) { return (K + GV_COLS - 1) / GV_COLS * (2 * GV_COLS) + GV_PAD; }
@@ -362,11 +363,14 @@ __device__ __forceinline__ void put(void* y, size_t i, float v) {
 
 // NT = 0: one token; otherwise NT blocks of eight. All of x in shared memory.
 template <int NT, int M, bool F32, bool WHOLE>
-__global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(const GemvParams p) {
+__global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(GemvParams p) {
     extern __shared__ __align__(16) unsigned char sm[];
     using P = Plan<NT, M>;
     constexpr bool ONE = P::ONE;
     constexpr int TOK = P::TOK, NA = P::NA, ROWS = P::ROWS, RING = P::SLOTS * P::SLOT;
+    p.x += size_t(blockIdx.y) * p.share * p.K;
+    p.y = static_cast<char*>(p.y) + size_t(blockIdx.y) * p.share * p.N * (F32 ? 4 : 2);
+    p.T = min(p.share, p.T - int(blockIdx.y) * p.share);
     const int steps = (p.K + P::COLS - 1) / P::COLS, slices = (p.K + GV_COLS - 1) / GV_COLS, stride = row_stride(p.K);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int g = lane >> 2, q = lane & 3;
@@ -507,16 +511,17 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     return a && b && x < y + bn && y < x + an;
 }
 
-// One pass over W for p.T tokens.
+// Every p.share tokens a pass over W.
 template <int NT, int M, bool F32, bool WHOLE>
 bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
     using P = Plan<NT, M>;
-    const int fixed = P::fixed_bytes(p.T, p.K), room = (di.max_smem_optin - fixed) / P::WARP_BYTES;
+    const int fixed = P::fixed_bytes(p.share, p.K), room = (di.max_smem_optin - fixed) / P::WARP_BYTES;
     const int warps = room < P::WARPS ? room : P::WARPS, smem = fixed + warps * P::WARP_BYTES;
     const auto kern = gemv_kernel<NT, M, F32, WHOLE>;
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return false;
     const int tiles = (p.N + P::ROWS - 1) / P::ROWS;
-    return launch(kern, dim3(tiles < di.sm_count ? tiles : di.sm_count), 32 * warps, smem, stream, 1, p);
+    const dim3 grid(tiles < di.sm_count ? tiles : di.sm_count, (p.T + p.share - 1) / p.share);
+    return launch(kern, grid, 32 * warps, smem, stream, 1, p);
 }
 
 // Whether up to eight tokens take steps of two tiles: where all warps' rings fit beside x (24571 x
@@ -526,7 +531,7 @@ bool launch_gemv(const GemvParams& p, const DevInfo& di, cudaStream_t stream) {
 // more rows (2048 x 4096, 32 instead of 16: 7.7 against 6.7 us at T = 4).
 bool two_tiles(const GemvParams& p, const DevInfo& di) {
     using P = Plan<1, 2>;
-    if (P::fixed_bytes(p.T, p.K) + P::WARPS * P::WARP_BYTES > di.max_smem_optin) return false;
+    if (P::fixed_bytes(p.share, p.K) + P::WARPS * P::WARP_BYTES > di.max_smem_optin) return false;
     const int t1 = (p.N + 15) / 16, t2 = (p.N + 31) / 32, sms = di.sm_count;
     return t2 > sms && 20 * ((t2 + sms - 1) / sms) <= 11 * ((t1 + sms - 1) / sms);
 }
@@ -544,9 +549,9 @@ bool fits(int T, int K, int smem) {
 
 template <bool F32, bool WHOLE>
 bool launch_tokens(const GemvParams& p, const DevInfo& di, cudaStream_t s) {
-    if (p.T == 1) return launch_gemv<0, 1, F32, WHOLE>(p, di, s);
-    if (p.T <= 8) return two_tiles(p, di) ? launch_gemv<1, 2, F32, WHOLE>(p, di, s) : launch_gemv<1, 1, F32, WHOLE>(p, di, s);
-    if (p.T <= 16) return launch_gemv<2, 1, F32, WHOLE>(p, di, s);
+    if (p.share == 1) return launch_gemv<0, 1, F32, WHOLE>(p, di, s);
+    if (p.share <= 8) return two_tiles(p, di) ? launch_gemv<1, 2, F32, WHOLE>(p, di, s) : launch_gemv<1, 1, F32, WHOLE>(p, di, s);
+    if (p.share <= 16) return launch_gemv<2, 1, F32, WHOLE>(p, di, s);
     return launch_gemv<4, 1, F32, WHOLE>(p, di, s);
 }
 
@@ -578,18 +583,18 @@ extern "C" redmoe_status redmoe_gemv(const redmoe_matrix* W, const void* x, int3
     p.s = static_cast<const uint16_t*>(W->s);
     p.N = W->rows;
     p.K = W->cols;
-    // Token rows at a time: all, or an equal share of them that leaves room for eight rings.
-    int most = T;
-    for (int n = 2; most > 1 && !fits(most, p.K, di.max_smem_optin); ++n) most = (T + n - 1) / n;
+    // Token rows at a time: all, or an equal share of them that leaves room for eight rings. A matrix of few
+    // rows leaves multiprocessors free: as many shares as these can take at once (512 x 2048: 4.2 us at
+    // T = 8, all in one share 4.5, at T = 32 4.6 and 10.6; 512 x 7040 at T = 32 10.5, in turn 48.9).
+    p.T = T;
+    p.x = static_cast<const uint16_t*>(x);
+    p.y = y;
+    const int tiles = (p.N + 15) / 16, free = di.sm_count / tiles;
+    int n = free > 1 ? (free < T ? free : T) : 1;
+    while (p.share = (T + n - 1) / n, p.share > 1 && !fits(p.share, p.K, di.max_smem_optin)) ++n;
     const bool f32 = y_dtype == DT_F32, whole = p.K % GV_COLS == 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    for (int t = 0; t < T; t += most) {
-        p.T = T - t < most ? T - t : most;
-        p.x = static_cast<const uint16_t*>(x) + size_t(t) * p.K;
-        p.y = static_cast<char*>(y) + size_t(t) * p.N * (f32 ? 4 : 2);
-        const bool ok = f32 ? (whole ? launch_tokens<true, true>(p, di, st) : launch_tokens<true, false>(p, di, st))
-                            : (whole ? launch_tokens<false, true>(p, di, st) : launch_tokens<false, false>(p, di, st));
-        if (!ok) return REDMOE_ERR_CUDA;
-    }
-    return REDMOE_OK;
+    const bool ok = f32 ? (whole ? launch_tokens<true, true>(p, di, st) : launch_tokens<true, false>(p, di, st))
+                        : (whole ? launch_tokens<false, true>(p, di, st) : launch_tokens<false, false>(p, di, st));
+    return ok ? REDMOE_OK : REDMOE_ERR_CUDA;
 }

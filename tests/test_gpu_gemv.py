@@ -47,7 +47,8 @@ def test_sizes(gpu_lib, N, K, T, out):
 
 @pytest.mark.parametrize("N,K,T", [(33, 32768, 32), (16, 65536, 1), (24, 65536, 2), (40, 16384, 13), (9000, 256, 5),
                                    (40000, 128, 1), (40001, 64, 12), (70, 11008, 8), (70, 12000, 7), (90, 5376, 16),
-                                   (50, 2560, 31), (4800, 512, 4), (4740, 4096, 8)])
+                                   (50, 2560, 31), (4800, 512, 4), (4740, 4096, 8), (1100, 288, 7), (1200, 288, 9),
+                                   (600, 7040, 32)])
 def test_long_and_wide(gpu_lib, N, K, T):
     w, s, x = make(N, K, T)
     y = run(w, s, x)

@@ -225,6 +225,7 @@ template <int NT, int M_ = 1> struct Plan {
 template <class P>
 struct Cursor {
     static constexpr int LANES = 32 / P::ROWS ? 32 / P::ROWS : 1;  // lanes that share a row's scales
+    static constexpr int EACH = P::COLS / 32 / LANES;              // scales of a lane
     const uint8_t* w;
     const uint16_t* sc;
     int tile, s;
@@ -246,7 +247,8 @@ struct Cursor {
 // slices) or zeroed: what lies there need not be finite. WHOLE: K % 256 == 0, a row's scales of a
 // slice are 16 bytes.
 template <bool WHOLE, class P>
-__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<P>& c, int lane, unsigned char* slot) {
+__device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<P>& c, int lane, unsigned char* slot,
+                                      uint16_t (&later)[Cursor<P>::EACH]) {
     constexpr int SLICES = P::COLS / GV_COLS;
     const uint32_t dst = smem_u32(slot) + (lane / 8) * P::WROW + 16 * (lane % 8);
     const int groups = p.K / 32 - c.s * (P::COLS / 32);  // groups left in the row
@@ -265,20 +267,25 @@ __device__ __forceinline__ void fetch(const GemvParams& p, const Cursor<P>& c, i
                     cp_async16(dst + 4 * j * P::WROW + 128 * h, c.w + j * step4 + 128 * h);
         }
     }
-    unsigned char* ss = slot + P::ROWS * P::WROW + (lane % P::ROWS) * P::SROW;
-    if (full || c.tile * P::ROWS + lane % P::ROWS < p.N) {
-        const int h = lane / P::ROWS;  // the lanes that share a row take a slice each
-        if (WHOLE) {
-            if (h < SLICES && (h == 0 || groups > 8 * h)) cp_async16(smem_u32(ss) + 16 * h, c.sc + 8 * h);
-        } else {
-            constexpr int EACH = P::COLS / 32 / Cursor<P>::LANES;  // scales a lane fetches
+    const int h = lane / P::ROWS;  // the lanes that share a row take a slice or EACH scales each
+    const bool there = full || c.tile * P::ROWS + lane % P::ROWS < p.N;
+    if constexpr (WHOLE) {
+        if (there && h < SLICES && (h == 0 || groups > 8 * h))
+            cp_async16(smem_u32(slot + P::ROWS * P::WROW + (lane % P::ROWS) * P::SROW) + 16 * h, c.sc + 8 * h);
+    } else {
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) {
-                const int k = EACH * h + i;
-                reinterpret_cast<uint16_t*>(ss)[k] = k < groups ? c.sc[k] : uint16_t(0);
-            }
+        for (int i = 0; i < Cursor<P>::EACH; ++i) {
+            const int k = Cursor<P>::EACH * h + i;
+            later[i] = there && k < groups ? c.sc[k] : uint16_t(0);
         }
     }
+}
+// The scales that fetch left in registers, when their step begins.
+template <class P>
+__device__ __forceinline__ void settle(int lane, unsigned char* slot, const uint16_t (&later)[Cursor<P>::EACH]) {
+    uint16_t* to = reinterpret_cast<uint16_t*>(slot + P::ROWS * P::WROW + (lane % P::ROWS) * P::SROW);
+#pragma unroll
+    for (int i = 0; i < Cursor<P>::EACH; ++i) to[Cursor<P>::EACH * (lane / P::ROWS) + i] = later[i];
 }
 
 // One token, 16 rows by 256 columns: lane (g, q) reads chunk q + 4 (g & 1) of rows g / 2 + 4 j. The
@@ -392,9 +399,11 @@ __global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(GemvPa
     Cursor<P> in;
     in.at(p, ta + za / steps, za % steps, lane);
     int tile = in.tile, s = in.s, zin = za, sin = 0;
+    static_assert(P::SLOTS == 2, "`later` is one step's");
+    uint16_t later[Cursor<P>::EACH];
     auto ask = [&]() {  // one group per call, an empty one behind the last step
         if (zin < zb) {
-            fetch<WHOLE, P>(p, in, lane, ring + sin);
+            fetch<WHOLE, P>(p, in, lane, ring + sin, later);
             in.next(p, steps, lane);
             sin = sin + P::SLOT == RING ? 0 : sin + P::SLOT;
             ++zin;
@@ -459,6 +468,7 @@ __global__ void __launch_bounds__(32 * Plan<NT, M>::WARPS, 1) gemv_kernel(GemvPa
     int slot = 0;
     for (int z = za; z < zb; ++z) {
         cp_wait<P::SLOTS - 2>();
+        if (!WHOLE) settle<P>(lane, ring + slot, later);
         __syncwarp();
         const unsigned char *w = my_w + slot, *sc = my_s + slot;
         auto release = [&]() {

@@ -363,9 +363,10 @@ redmoe_status redmoe_norm_forward(const redmoe_norm *N, const void *h, const voi
  *   dgate    TOKEN: fp32 [T]; CHANNEL: fp32 [hidden]; ELEMENT: gate_dtype [T, hidden]; NULL:
  *            not wanted
  *   dpost_w, dpre_w   fp32 [hidden], 16-byte aligned; NULL: not wanted
- * Overwritten, not accumulated; sums over rows are fp32 in a fixed order. The workspace is
- * needed for dpost_w, dpre_w and a CHANNEL dgate (else it may be NULL); its control block is
- * not used. T == 0 zeroes those three and touches nothing else. */
+ * A row whose sum of squares passes the fp32 range (normalised to zero, see above) sends
+ * nothing back through its norm. Overwritten, not accumulated; sums over rows are fp32 in a
+ * fixed order. The workspace is needed for dpost_w, dpre_w and a CHANNEL dgate (else it may
+ * be NULL); its control block is not used. T == 0 zeroes those three and touches nothing else. */
 size_t redmoe_norm_workspace_bytes(const redmoe_norm *N, int32_t T);
 redmoe_status redmoe_norm_backward(const redmoe_norm *N, const void *h_out, const void *y, const void *gate,
                                    const void *dh_out, const void *dx, int32_t T, void *dh, void *dy, void *dgate,

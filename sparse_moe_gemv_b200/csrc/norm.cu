@@ -435,9 +435,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
         }
         group_sum6(s, red[turn][group], p.tpr, group, wig);
         turn ^= 1;
-        const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps)), k2 = r2 * r2 * (s[1] * p.inv_h);
+        // a norm whose row passes the fp32 range of its squares (r = 0) is constant there: it sends nothing
+        // back, and the other sums over that row may be infinite
+        const float r2 = rsqrtf(fmaf(s[0], p.inv_h, p.eps)), k2 = r2 == 0.0f ? 0.0f : r2 * r2 * (s[1] * p.inv_h);
         const float r1 = post_norm ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.0f;
-        const float sum = has_x ? fmaf(r2, fmaf(-k2, s[5], s[4]), s[3]) : s[3];  // of G e
+        float sum = has_x && r2 != 0.0f ? fmaf(r2, fmaf(-k2, s[5], s[4]), s[3]) : s[3];  // of G e
+        if (r1 == 0.0f) sum = 0.0f;
         const float k1 = post_norm ? r1 * r1 * (sum * p.inv_h) : 0.0f, f1 = r1 * kappa;
         if (tokens && p.dgate && lane == 0)
             static_cast<float*>(p.dgate)[t] = p.block_scale * dtoken * r1 * sum;
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward
                 F8 w = get_shared(post, p.chunks, c);
                 if (element) {
                     if (p.dgate) {
-                        F8 dg = mul(mul(mul(G, y), f1), w);
+                        F8 dg = mul(mul(G, mul(y, f1)), w);
                         if (p.sigmoid) dg = mul(dg, sigmoid_slope(read_gate(at + i * chunk_bytes)));
                         if (p.gate_f32) store8<DT_F32>(p.dgate, row + c, dg);
                         else store8<DT_BF16>(p.dgate, row + c, dg);

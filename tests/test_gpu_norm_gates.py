@@ -1,4 +1,4 @@
-"""Gradients of sigmoid gates far from zero.
+"""Gradients of sigmoid gates far from zero, and of rows beyond the fp32 range of their squares.
 
 Tolerance: as in test_gpu_norm.py, 256 U of a gradient's magnitude for gates of order one. The slope
 of the logistic function at a, s(a) s(-a), adds what rounding the exponent |a| log2(e) costs: the
@@ -62,3 +62,36 @@ def test_an_infinite_gate_has_no_slope(gpu_lib):
     t["gate"][0, 3], t["gate"][1, 5], t["gate"][2, 7] = float("inf"), -float("inf"), float("nan")
     o = backward(norm, t, 3, 256)
     assert float(o["dgate"][0, 3]) == 0.0 and float(o["dgate"][1, 5]) == 0.0 and bool(o["dgate"][2, 7].isnan())
+
+
+@pytest.mark.parametrize("T,H,kind", [(6, 512, "none"), (6, 512, "token"), (6, 512, "element"), (6, 4104, "channel"),
+                                      (700, 2048, "channel")])
+@pytest.mark.parametrize("size", [1e25, 3e38])
+def test_rows_beyond_the_range_of_their_squares(gpu_lib, T, H, kind, size):
+    """Forward normalises such a row to zero, whatever it holds: a norm that is constant there sends
+    nothing back, and the rows beside it keep their gradients."""
+    norm, t, kw = make(T, H, h="f32", x="f32", w="f32", y="f32", post=True, kind=kind)
+    t["h"][1] = size
+    t["y"][3] = size
+    t["dx"][1] = t["dx"][1].abs() + 1.0  # sums of one sign, which overflow too
+    t["dh_out"][3] = t["dh_out"][3].abs() + 1.0
+    t["h"][4] = size
+    t["y"][4] = -size
+    o = backward(norm, t, T, H)
+    assert all(not v.isnan().any() for v in o.values())
+    assert torch.equal(o["dh"][1], t["dh_out"][1]) and torch.equal(o["dh"][4], t["dh_out"][4])
+    assert float(o["dy"][3].abs().max()) == 0.0 and float(o["dy"][4].abs().max()) == 0.0
+    keep = [i for i in range(T) if i not in (1, 3, 4)]
+    rest = {n: v if v is None or v.shape[:1] != (T,) else v[keep].contiguous() for n, v in t.items()}
+    ref = NormCase(rest["h"], rest["y"], rest["gate"], rest["pre_w"], rest["post_w"], **kw).backward(rest["dh_out"], rest["dx"])
+    for n in ("dh", "dy"):
+        close(n, o[n][keep], ref[n][0], 256 * U * ref[n][1])
+    # row 1 reaches the sums over rows through y, row 3 through h, row 4 not at all
+    zero_h, zero_y = t["h"].double().cpu(), t["y"].double().cpu()
+    zero_h[[1, 4]] = 0.0
+    zero_y[[3, 4]] = 0.0
+    dxs = t["dx"].clone()
+    dxs[[1, 4]] = 0.0
+    ref = NormCase(zero_h, zero_y, t["gate"], t["pre_w"], t["post_w"], **kw).backward(t["dh_out"], dxs)
+    for n in ("dpre_w", "dpost_w") + (("dgate",) if kind == "channel" else ()):
+        close(n, o[n], ref[n][0], 256 * U * ref[n][1])

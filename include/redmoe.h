@@ -378,10 +378,12 @@ redmoe_status redmoe_norm_backward(const redmoe_norm *N, const void *h_out, cons
  * `before` is used as in redmoe_norm_forward with y == NULL, `after` as with y. Both have
  * the layer's hidden; before->x_dtype is the layer's x_dtype, after->y_dtype is REDMOE_F32
  * (the layer's output) and after->h_dtype is before->h_dtype; otherwise
- * REDMOE_ERR_INVALID_ARG. h_out may be h itself, x_next may be NULL. Sizes, ids, weights
- * and statuses as redmoe_forward; the workspace holds redmoe_workspace_bytes_block(L, T)
- * bytes. If the layer's own dispatch refuses the layer (REDMOE_ERR_UNSUPPORTED) or a launch
- * fails, the first norm may have been enqueued: it writes the workspace only. */
+ * REDMOE_ERR_INVALID_ARG. h_out may be h itself, x_next may be NULL; otherwise no output, and
+ * not the workspace, may overlap h, gate or a norm's weight (REDMOE_ERR_INVALID_ARG). Sizes,
+ * ids, weights and statuses as redmoe_forward; the workspace holds
+ * redmoe_workspace_bytes_block(L, T) bytes. If the layer's own dispatch refuses the layer
+ * (REDMOE_ERR_UNSUPPORTED) or a launch fails, the first norm may have been enqueued: it writes
+ * the workspace only. */
 size_t redmoe_workspace_bytes_block(const redmoe_layer *L, int32_t T);
 redmoe_status redmoe_forward_block(const redmoe_layer *L, const redmoe_norm *before, const redmoe_norm *after,
                                    const void *h, const void *gate, int32_t T, void *h_out, void *x_next,

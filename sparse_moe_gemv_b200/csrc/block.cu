@@ -71,6 +71,14 @@ redmoe_status redmoe_forward_block(const redmoe_layer* L, const redmoe_norm* bef
     }
     if ((st = norm_forward_check(before, h, nullptr, nullptr, T, nullptr, base + b.x)) != REDMOE_OK) return st;
     if ((st = norm_forward_check(after, h, base + b.out, gate, T, h_out, x_next)) != REDMOE_OK) return st;
+    // the second norm reads behind the layer, whose ids, weights and workspace must leave its inputs alone
+    const struct { const void* p; size_t n; } in[] = {{gate, norm_gate_bytes(after, T)},
+                                                      {before->pre_w, norm_weight_bytes(before)},
+                                                      {after->pre_w, norm_weight_bytes(after)},
+                                                      {after->post_w, norm_weight_bytes(after)}};
+    for (const auto& o : out)
+        for (const auto& r : in)
+            if (overlap(o.p, o.n, r.p, r.n)) return REDMOE_ERR_INVALID_ARG;
     if ((st = redmoe_norm_forward(before, h, nullptr, nullptr, T, nullptr, base + b.x, stream)) != REDMOE_OK) return st;
     st = redmoe_forward(L, base + b.x, T, reinterpret_cast<float*>(base + b.out), topk_ids, topk_w, workspace,
                         workspace_bytes, nullptr, stream);

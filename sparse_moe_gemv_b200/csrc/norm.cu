@@ -694,12 +694,12 @@ redmoe_status norm_forward_check(const redmoe_norm* N, const void* h, const void
     if (branch ? !h_out : (h_out || !x || gate)) return REDMOE_ERR_INVALID_ARG;
     if (branch && (N->gate_kind != GATE_NONE) != (gate != nullptr)) return REDMOE_ERR_INVALID_ARG;
     if (gate && !aligned(gate, N->gate_kind == GATE_TOKEN ? dt_bytes(N->gate_dtype) : 16)) return REDMOE_ERR_INVALID_ARG;
-    const size_t n = size_t(T) * N->hidden, wb = dt_bytes(N->w_dtype) * N->hidden;
+    const size_t n = size_t(T) * N->hidden, wb = norm_weight_bytes(N);
     const Range rh{static_cast<const char*>(h), n * dt_bytes(N->h_dtype)};
     const Range ro{static_cast<const char*>(h_out), n * dt_bytes(N->h_dtype)};
     const Range rx{static_cast<const char*>(x), n * dt_bytes(N->x_dtype)};
     const Range in[] = {{static_cast<const char*>(y), n * dt_bytes(N->y_dtype)},
-                        {static_cast<const char*>(gate), gate_elems(N, T) * dt_bytes(N->gate_dtype)},
+                        {static_cast<const char*>(gate), norm_gate_bytes(N, T)},
                         {static_cast<const char*>(N->pre_w), wb},
                         {static_cast<const char*>(N->post_w), wb}};
     for (const Range& r : in)
@@ -707,6 +707,9 @@ redmoe_status norm_forward_check(const redmoe_norm* N, const void* h, const void
     if (overlap(rh, rx) || overlap(ro, rx) || (h_out != h && overlap(rh, ro))) return REDMOE_ERR_INVALID_ARG;
     return REDMOE_OK;
 }
+
+size_t norm_gate_bytes(const redmoe_norm* N, int T) { return gate_elems(N, T) * dt_bytes(N->gate_dtype); }
+size_t norm_weight_bytes(const redmoe_norm* N) { return dt_bytes(N->w_dtype) * N->hidden; }
 
 }  // namespace redmoe
 

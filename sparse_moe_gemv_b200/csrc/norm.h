@@ -9,4 +9,8 @@ namespace redmoe {
 redmoe_status norm_forward_check(const redmoe_norm* N, const void* h, const void* y, const void* gate, int T,
                                  const void* h_out, const void* x);
 
+// Bytes of a gate for T rows, and of one weight.
+size_t norm_gate_bytes(const redmoe_norm* N, int T);
+size_t norm_weight_bytes(const redmoe_norm* N);
+
 }  // namespace redmoe

@@ -473,6 +473,14 @@ def _int32(n: int, name: str) -> int:
     return n
 
 
+def _rows(t: torch.Tensor, name: str) -> int:
+    """T of a tensor whose first dimension is the token rows (its shape is checked beside the others')."""
+    shape = t.shape
+    if not shape:
+        raise ValueError(f"{name}: expected rows of tokens, got a scalar")
+    return shape[0] if shape[0] <= _INT32_MAX else _int32(shape[0], "T")
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -591,7 +599,7 @@ def redmoe_norm_backward(norm: Norm, h_out: torch.Tensor, dh: torch.Tensor, work
     if dev != _raw_device():
         return _elsewhere(dev, redmoe_norm_backward, norm, h_out, dh, workspace, dh_out, dx, y, gate, dy, dgate, dpost_w,
                           dpre_w, stream)
-    T = _int32(h_out.size(0), "T")
+    T = _rows(h_out, "h_out")
     rows, cols, f32, ht = (T, norm.hidden), (norm.hidden,), torch.float32, norm.h_torch
     g = dg = None
     if gate is not None:
@@ -634,7 +642,7 @@ def redmoe_forward_block(layer: Layer, before: Norm, after: Norm, h: torch.Tenso
     if dev != _raw_device():
         return _elsewhere(dev, redmoe_forward_block, layer, before, after, h, h_out, topk_ids, topk_w, workspace, x_next,
                           gate, stream)
-    T = _int32(h.size(0), "T")
+    T = _rows(h, "h")
     for name, t in layer.tensors.items():
         if t is not None and t.get_device() != dev:
             raise ValueError(f"the layer's {name} is on {t.device}, h on cuda:{dev}")
@@ -740,12 +748,10 @@ def redmoe_gemv(matrix: Matrix, x: torch.Tensor, y: torch.Tensor, stream=None) -
     dev = matrix.device
     if dev != _raw_device():
         return _elsewhere(dev, redmoe_gemv, matrix, x, y, stream)
-    xt, yt, T = x.dtype, y.dtype, x.size(0)
+    xt, yt, T = x.dtype, y.dtype, _rows(x, "x")
     xc, yc = _CODES.get(xt), _CODES.get(yt)
     if xc is None or yc is None:
         raise ValueError(f"x and y are float32 or bfloat16: got {xt} and {yt}")
-    if T > _INT32_MAX:
-        _int32(T, "T")
     st = (_lib or load()).redmoe_gemv(matrix.ref, _arg(x, "x", (T, matrix.cols), xt, dev), xc, T,
                                       _arg(y, "y", (T, matrix.rows), yt, dev), yc,
                                       _raw_stream(dev) if stream is None else _stream(stream))

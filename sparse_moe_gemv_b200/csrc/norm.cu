@@ -668,14 +668,19 @@ NormKernel pick_backward(const redmoe_norm* N, int nc, int threads, bool branch)
 
 int units(int dt) { return dt == DT_F32 ? 2 : 1; }
 
-// Shared memory of a kernel that walks rows, and with it p.ahead: two rows in flight where `want`
-// blocks of an SM can hold them, else one, else none.
-int rows_smem(NormParams& p, const NormShape& s, int want, int max_smem) {
+// Shared memory of a kernel that walks rows, and with it p.ahead: two rows in flight where `want` blocks
+// of an SM can hold them, else one, else none. Where two blocks cannot even hold the row that each works
+// on, `want` becomes one block, which then has rows in flight (4096 fp32 rows of 4096 with an fp32 element
+// gate: 156 us, 194 as two waves of blocks). Two blocks without a row in flight stay: 8192 fp32 rows of 2048
+// take 107 us, one block with rows ahead 116; 4096 x 4096 bf16 with an fp32 y 65 and 69 (but 300 such rows
+// 15.6 and 14.3).
+int rows_smem(NormParams& p, const NormShape& s, int& want, int max_smem) {
     const int stage = s.nc * p.units * s.tpr * s.rows * 16, fixed = 2 * p.H * 4;
     const int own = 2 * (s.tpr * s.rows > 256 ? 1 : 8) * RED6 * 4 + 64;  // static
-    const int room = max_smem / want - own - (want > 1 ? 1024 : 0);      // 1 KiB of every block is the system's
+    auto room = [&] { return max_smem / want - own - (want > 1 ? 1024 : 0); };  // 1 KiB of every block is the system's
+    if (fixed + stage > room()) want = 1;
     p.ahead = 2;
-    while (p.ahead > 0 && fixed + (p.ahead + 1) * stage > room) --p.ahead;
+    while (p.ahead > 0 && fixed + (p.ahead + 1) * stage > room()) --p.ahead;
     const int smem = fixed + (p.ahead + 1) * stage, ends = (s.rows - 1) * 2 * p.H * 4;
     return smem > ends ? smem : ends;
 }
@@ -814,7 +819,11 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
     p.want_pre = dpre_w != nullptr;
     p.want_post = dpost_w != nullptr;
     p.want_gate = dgate != nullptr && channel;
-    const int threads = s.tpr * s.rows, want = threads <= 256 ? MAX_BLOCKS_SM : 1;
+    p.units = 2 * units(N->h_dtype) + units(N->x_dtype) + (branch ? units(N->y_dtype) : 0) +
+              (branch && N->gate_kind == GATE_ELEMENT ? units(N->gate_dtype) : 0);
+    const int threads = s.tpr * s.rows;
+    int want = threads <= 256 ? MAX_BLOCKS_SM : 1;
+    const int smem = rows_smem(p, s, want, di.max_smem_optin);
     const long long all = (T + (long long)s.rows - 1) / s.rows, most = want * (di.sm_count < MAX_SMS ? di.sm_count : MAX_SMS);
     // Where eight blocks have no more than two of their rows each, they are one cluster that adds its
     // column sums itself: 4.2 against 4.7 us for one row of 2048, and a launch less for the host (about
@@ -825,9 +834,6 @@ redmoe_status redmoe_norm_backward(const redmoe_norm* N, const void* h_out, cons
         blocks = 1;
         while (blocks < all && blocks < MAX_CLUSTER) blocks *= 2;  // those without rows add zeros
     }
-    p.units = 2 * units(N->h_dtype) + units(N->x_dtype) + (branch ? units(N->y_dtype) : 0) +
-              (branch && N->gate_kind == GATE_ELEMENT ? units(N->gate_dtype) : 0);
-    const int smem = rows_smem(p, s, want, di.max_smem_optin);
     const NormKernel kern = pick_backward(N, s.nc, threads, branch);
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return REDMOE_ERR_CUDA;
     if (!launch(kern, dim3(blocks), threads, smem, stm, p.cluster ? blocks : 1, p)) return REDMOE_ERR_CUDA;

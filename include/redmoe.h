@@ -23,8 +23,9 @@
  * Conventions for every entry point:
  *  - Every tensor pointer is DEVICE memory owned by the caller; the library allocates
  *    no memory and keeps no state between calls except a per-device cache of device
- *    attributes and the fixed scratch array of redmoe_forward_noalloc (static memory in
- *    the library image). Tensors are dense, row-major, contiguous.
+ *    attributes and of kernels' shared-memory limits, and the fixed scratch array of
+ *    redmoe_forward_noalloc (static memory in the library image). Tensors are dense,
+ *    row-major, contiguous.
  *  - `stream` is a cudaStream_t (NULL: the legacy default stream). Work is only
  *    enqueued; no call synchronises the host except redmoe_check_timeout().
  *  - Arguments are validated on the host before anything is enqueued. On any error
@@ -316,8 +317,9 @@ redmoe_status redmoe_forward_noalloc(const redmoe_layer *L, const void *x, int32
  * [T, hidden] (ELEMENT), act the identity (LINEAR) or the logistic function (SIGMOID).
  * Statistics are fp32 (a row whose sum of squares passes the fp32 range is normalised to zero
  * where it is finite); x is computed from h_out before h_out is rounded to h_dtype, so
- * every output is rounded once. Rows are independent; T = 1 and long batches run the same
- * kernel. hidden is a multiple of 8 up to 8192 (more: REDMOE_ERR_UNSUPPORTED); dtypes are
+ * every output is rounded once. Rows are independent: what one holds does not reach another. The
+ * order of a row's sums is fixed for given sizes, but depends on T and the device as well as on
+ * hidden: the same row may differ in its last bits between a short call and a long one. hidden is a multiple of 8 up to 8192 (more: REDMOE_ERR_UNSUPPORTED); dtypes are
  * REDMOE_F32 or REDMOE_BF16; tensors are 16-byte aligned (a TOKEN gate: to its element).
  * These operators are this library's own: the pages describe the layers around the MoE
  * block only by name ("Architecture", "Qwen3-Next shape"). */
@@ -408,10 +410,12 @@ redmoe_status redmoe_forward_block(const redmoe_layer *L, const redmoe_norm *bef
  * dlogits has the logits' dtype, is overwritten and may be logits itself. counts and n_rows
  * are those of the forward call. E is 1..1024, k 1..min(E, 32), T k at most 2^30; logits
  * REDMOE_F32 or REDMOE_BF16, 16-byte aligned. Sums over rows have a fixed order: results do
- * not depend on timing. Outputs must not overlap inputs or one another
+ * not depend on timing. They are fp32 over the rows that one warp adds, then over warps and
+ * blocks: prob and the losses' sums are off by at most about (256 + T / R) 2^-24 of themselves,
+ * R = 9472 up to 128 experts and 2368 beyond on a device of 148 multiprocessors. Outputs must not overlap inputs or one another
  * (REDMOE_ERR_INVALID_ARG). The workspace holds redmoe_balance_workspace_bytes(T, E) bytes;
- * its control block is not used. T == 0 writes zeros forward and nothing backward. This library's own; the pages describe
- * inference only. */
+ * its control block is not used. T == 0 writes zeros forward and nothing backward. This
+ * library's own; the pages describe inference only. */
 size_t redmoe_balance_workspace_bytes(int32_t T, int32_t E);
 redmoe_status redmoe_balance_forward(const void *logits, int32_t logits_dtype, const int32_t *topk_ids,
                                      const uint8_t *row_mask, int32_t T, int32_t E, int32_t k, float *loss,
@@ -427,11 +431,12 @@ redmoe_status redmoe_balance_backward(const void *logits, int32_t logits_dtype, 
  * REDMOE_ERR_UNSUPPORTED). W is REDMOE_INT4G32 (others: REDMOE_ERR_UNSUPPORTED), x
  * REDMOE_BF16 [T, cols], y REDMOE_F32 or REDMOE_BF16 [T, rows], overwritten, aligned to its
  * element. cols is a multiple of 32 up to 65536. Products are exact (but for elements of x under
- * 2^-116 of their row's largest), sums are fp32 in an order that is fixed for given sizes; their
- * rounding is in proportion to 16 times the sum of |scale x|, since they run over the stored
- * nibbles 0 .. 15. A row of x that holds an infinity or a NaN makes its row of y NaN; other rows
- * are not affected. W is read once for all rows of x if they fit on a multiprocessor (at T = 8
- * up to 10752 columns, at 16 up to 5120, at 32 up to 2304), else, and where a matrix of few rows leaves
+ * 2^-116 of their row's largest), sums are fp32 in an order that is fixed for given sizes and in
+ * units of the row's largest x, which takes scales of 0 and of 2^-100 .. 2^114. Their rounding is
+ * in proportion to 16 times the sum of |scale x|, since they run over the stored nibbles 0 .. 15.
+ * A row of x that holds an infinity or a NaN makes its row of y NaN; other rows are not affected.
+ * W is read once for all rows of x if they fit on a multiprocessor (at T = 8 up to 10752 columns,
+ * at 16 up to 5120, at 32 up to 2304), else, and where a matrix of few rows leaves
  * multiprocessors free, once for every equal share of them. y must not overlap x or W. */
 typedef struct redmoe_matrix {
     int32_t rows;            /* N                                                             */

@@ -195,7 +195,8 @@ __device__ __forceinline__ void shape_x(const GemvParams& p, const RowShare& sh,
 
 // What a pass over NT blocks of eight tokens, or (NT = 0) over one token, uses. Two tokens already
 // take the block of eight: 18.5 us where a kernel for two like the one for one took 20.6 (24571 x
-// 4096). Each number against its neighbours, in us:
+// 4096). Each number against its neighbours, in us, the two sides of a choice in one state of the kernel (later
+// steps moved both: compare within a line only):
 //   M      two tiles a step up to eight tokens, see two_tiles; with more blocks of eight, steps of two
 //          tiles of 256 or 128 columns take 31.9 and 29.7, one tile 24.5 (T = 13, 24571 x 4096)
 //   WARPS  20 and 16: 34.2 (T = 1, 151936 x 2048) and 16.4 (T = 4); 12 warps 37.8 and 18.0

@@ -140,8 +140,9 @@ __device__ __forceinline__ F8 sigmoid_slope(const F8& a) {
 }
 
 // One row per group of p.tpr threads; NC chunks a thread (chunk c = thread + i tpr). Everything a
-// row needs is asked for before the first sum waits. 64 registers a thread: 76 without a spill, and so
-// fewer blocks on an SM, take 28.1 instead of 25.7 us for 8192 rows of 2048.
+// row needs is asked for before the first sum waits. 64 registers a thread,
+// at which the two-chunk forms with a block output spill 8 to 28 bytes: 76 without a spill, and so fewer blocks
+// on an SM, take 28.1 instead of 25.7 us for 8192 rows of 2048.
 template <int HD, int YD, int XD, int NC, bool BRANCH>
 __global__ void __launch_bounds__(512, 2) norm_forward_kernel(const NormParams p) {
     constexpr bool EARLY = NC == 1;  // the weights too, where registers allow

@@ -69,3 +69,18 @@ def test_runs_of_masked_rows_between_live_ones(gpu_lib, E, dtype):
     rd, md = balance_backward(logits, counts, rn, k, GRAD, mask)
     bad = (dl.double() - rd).abs() - store_tol(rd, 128 * U * md, dl.dtype)
     assert not dl.isnan().any() and float(bad.max()) <= 0
+
+
+@pytest.mark.parametrize("T,E,dtype", [(2000003, 20, "f32"), (700001, 130, "bf16")])
+def test_sums_over_many_equal_rows(gpu_lib, T, E, dtype):
+    """Equal rows round their sums in one direction: the bound of (256 + T / R) U still holds."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    row = torch.randn(1, E, generator=g, device="cuda").to(smg.TORCH_DTYPES[dtype])
+    logits, ids = row.expand(T, E).contiguous(), torch.full((T, 1), 3, device="cuda", dtype=torch.int32)
+    loss, counts, prob, n, _ = (v.cpu() for v in run(logits, ids, None, GRAD))
+    rl, _, rp, _, mag = balance_forward(row, ids[:1])
+    bound = (256 + T / (9472 if E <= 128 else 2368)) * U
+    assert int(n) == T and int(counts[3]) == T and int(counts.sum()) == T
+    assert bool(((prob.double() - rp).abs() <= store_tol(rp, bound * rp, torch.float32)).all())
+    assert bool(((loss.double() - rl).abs() <= store_tol(rl, bound * mag, torch.float32)).all())

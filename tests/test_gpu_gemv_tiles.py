@@ -26,3 +26,16 @@ def test_two_tiles_a_step(gpu_lib, N, K, T, out):
 def test_one_tile_a_step_of_many_rows(gpu_lib, N, K, T, out):
     w, s, x = make(N, K, T)
     check(w, s, x, run(w, s, x, out))
+
+
+@pytest.mark.parametrize("T", [1, 5, 13])
+@pytest.mark.parametrize("power", [-100, 113])
+def test_scales_at_both_ends(gpu_lib, T, power):
+    """A group's sum is at most 4 in units of its row's largest x, so 2^114 over all of 2048 groups still
+    fits, and the roundings of subnormal partial sums stay under the bound from 2^-100 on."""
+    w, s, x = make(40, 512, T)
+    s = torch.full_like(s, 2.0 ** power)
+    s[::3, 1] = 0.0
+    check(w, s, x, run(w, s, x))
+    tiny = (x.float() * 2.0 ** -100).to(torch.bfloat16) if power > 0 else (x.float() * 2.0 ** 60).to(torch.bfloat16)
+    check(w, s, tiny, run(w, s, tiny))
